@@ -15,7 +15,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "librssm.so")
-SOURCES = ["rssm_kernels.cu", "rssm_api.cu", "rssm_stage.cu"]
+SOURCES = ["rssm_kernels.cu", "rssm_api.cu", "rssm_scan.cu", "rssm_stage.cu", "rssm_stage_prompt.cu"]
 HEADERS = ["rssm_device.cuh", "rssm_internal.h", "rssm_mma.cuh"]
 
 NVCC_FLAGS = [

@@ -6,6 +6,8 @@
 // except rssm_get_error, which waits for its stream.
 #include <cuda_runtime.h>
 
+#include <initializer_list>
+
 #include "rssm.h"
 #include "rssm_internal.h"
 
@@ -69,6 +71,13 @@ rssm_status_t check_state_fields(const rssm_desc_t* d, const rssm_state_t* st, b
 
 rssm_status_t check_state_common(const rssm_desc_t* d, const rssm_state_t* st) {
     return check_state_fields(d, st, true);
+}
+
+// The prompt calls read and write 16 bytes at a time.
+bool aligned16(std::initializer_list<const void*> ps) {
+    for (const void* p : ps)
+        if (reinterpret_cast<uintptr_t>(p) & 15u) return false;
+    return true;
 }
 
 }  // namespace
@@ -285,6 +294,49 @@ rssm_status_t rssm_prefill(const rssm_desc_t* d, const rssm_state_t* st, int32_t
     a.dt = dt;
     a.A = A;
     return cuda_status(launch_prefill(a, d->in_dtype == RSSM_BF16, static_cast<cudaStream_t>(stream)));
+}
+
+size_t rssm_prefill_scan_workspace_bytes(const rssm_desc_t* d, int32_t total, int32_t max_seqlen) {
+    if (rssm_check_desc(d) != RSSM_OK || total <= 0 || max_seqlen <= 0) return 0;
+    const Shape s = shape_of(d);
+    return scan_workspace_bytes(s, total, scan_segment_len(s, d->in_dtype == RSSM_BF16, total, max_seqlen));
+}
+
+rssm_status_t rssm_prefill_scan(const rssm_desc_t* d, const rssm_state_t* st, int32_t total, int32_t max_seqlen,
+                                const int32_t* cu_seqlens, const void* x, const void* B, const void* C,
+                                const float* dt, const float* A, const float* D, float* y, void* workspace,
+                                size_t workspace_bytes, void* stream) {
+    rssm_status_t s = rssm_check_desc(d);
+    if (s != RSSM_OK) return s;
+    if (d->update_dtype != RSSM_F32 || d->out_copy != RSSM_OUTCOPY_NONE) return RSSM_ERR_UNSUPPORTED;
+    if (!st || !st->record || !st->pos || !st->err || !cu_seqlens) return RSSM_ERR_INVALID_ARG;
+    if (total < 0 || max_seqlen < 0) return RSSM_ERR_INVALID_ARG;
+    if (total > 0 && (!x || !B || !C || !dt || !A || !D || !y)) return RSSM_ERR_INVALID_ARG;
+    if (!aligned16({x, B, C, dt, A, D, y, workspace})) return RSSM_ERR_INVALID_ARG;
+    if (total == 0) return RSSM_OK;
+    const size_t need = rssm_prefill_scan_workspace_bytes(d, total, max_seqlen);
+    if (need > 0 && !workspace) return RSSM_ERR_INVALID_ARG;
+    if (workspace_bytes < need) return RSSM_ERR_CAPACITY;
+    const int bf16 = d->in_dtype == RSSM_BF16;
+    ScanArgs a;
+    a.s = shape_of(d);
+    a.total = total;
+    a.max_seqlen = max_seqlen;
+    a.seg_len = max_seqlen > 0 ? scan_segment_len(a.s, bf16, total, max_seqlen) : 0;
+    a.cu = cu_seqlens;
+    a.rec = rec_of(d);
+    a.record = static_cast<unsigned char*>(st->record);
+    a.pos = st->pos;
+    a.err = st->err;
+    a.x = x;
+    a.B = B;
+    a.C = C;
+    a.dt = dt;
+    a.A = A;
+    a.D = D;
+    a.y = y;
+    a.ws = static_cast<float*>(workspace);
+    return cuda_status(launch_scan(a, bf16, static_cast<cudaStream_t>(stream)));
 }
 
 static rssm_status_t conv_launch(const rssm_desc_t* d, float* h, const int32_t* cur, int ntok, int32_t* err,

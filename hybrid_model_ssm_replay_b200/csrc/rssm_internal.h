@@ -111,6 +111,27 @@ struct PrefillArgs {
     const float* A;
 };
 
+// Selective scan of packed prompts with outputs. seg_len > 0: prompts are cut
+// into segments of that many tokens, and `ws` holds per segment slot (see
+// rssm_scan.cu) its state [H][P][N], then per slot and head its dt sum.
+struct ScanArgs {
+    Shape s;
+    int total, max_seqlen, seg_len;
+    const int32_t* cu;
+    RecLayout rec;
+    unsigned char* record;
+    const int32_t* pos;
+    int32_t* err;
+    const void* x;
+    const void* B;
+    const void* C;
+    const float* dt;
+    const float* A;
+    const float* D;
+    float* y;
+    float* ws;
+};
+
 // Conventional step / verify (s1, s3: the scheme ReplaySSM replaces).
 struct ConvArgs {
     Shape s;
@@ -132,11 +153,16 @@ struct ConvArgs {
 cudaError_t launch_replay(const ReplayArgs& a, int in_bf16, int read_fmt, cudaStream_t st);
 cudaError_t launch_fold(const FoldArgs& a, int in_bf16, int upd_fmt, cudaStream_t st);
 cudaError_t launch_prefill(const PrefillArgs& a, int in_bf16, cudaStream_t st);
+cudaError_t launch_scan(const ScanArgs& a, int in_bf16, cudaStream_t st);
 cudaError_t launch_conv(const ConvArgs& a, int in_bf16, int verify, cudaStream_t st);
 cudaError_t launch_accept(int batch, int K, int cap, const int32_t* n, int32_t* pos, int32_t* err, int add_one,
                           cudaStream_t st);
 cudaError_t launch_round_test(int op, int64_t n, const float* v, uint64_t seed, uint32_t c1, uint32_t c2,
                               uint32_t c3, void* out, cudaStream_t st);
+
+// Segment length of a scan (0: prompts run whole) and the workspace it needs.
+int scan_segment_len(const Shape& s, int in_bf16, int total, int max_seqlen);
+size_t scan_workspace_bytes(const Shape& s, int total, int seg_len);
 
 // Scratch of the no-allocation decode entry point (see rssm.h).
 uint32_t* noalloc_arrive_scratch();

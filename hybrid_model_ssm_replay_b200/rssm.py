@@ -22,7 +22,7 @@ RSSM_F32, RSSM_BF16, RSSM_E4M3, RSSM_FP4 = 0, 1, 2, 3
 RSSM_OUTCOPY_NONE, RSSM_OUTCOPY_FP4 = 0, 1
 RSSM_FLAG_FUSED_FLUSH = 1
 DEVERR = {0: "none", 1: "pos out of range", 2: "buffer capacity", 3: "accepted count out of range",
-          4: "bulk copy timeout"}
+          4: "bulk copy timeout", 5: "cu_seqlens out of range"}
 
 (FIELD_RECORD, FIELD_CKPT, FIELD_BBUF, FIELD_POS, FIELD_FLUSH_COUNT, FIELD_ARRIVE, FIELD_ERR) = range(7)
 
@@ -76,6 +76,8 @@ def lib():
         "rssm_accept": ([D, S, vp, vp], ct.c_int),
         "rssm_lowprec_refresh": ([D, S, vp, i32, vp], ct.c_int),
         "rssm_prefill": ([D, S, i32, vp, vp, vp, vp, vp], ct.c_int),
+        "rssm_prefill_scan": ([D, S, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, ct.c_size_t, vp], ct.c_int),
+        "rssm_prefill_scan_workspace_bytes": ([D, i32, i32], ct.c_size_t),
         "rssm_conv_step": ([D, vp, vp, vp, vp, vp, vp, vp, vp, vp], ct.c_int),
         "rssm_conv_verify": ([D, vp, vp, i32, vp, vp, vp, vp, vp, vp, vp, vp], ct.c_int),
         "rssm_conv_accept": ([D, vp, vp, i32, vp, vp], ct.c_int),
@@ -111,6 +113,21 @@ def _ptr(t, dtype=None, name="tensor"):
     if dtype is not None and t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
     return ct.c_void_p(t.data_ptr())
+
+
+def _arg(t, dtype, shape, name):
+    """_ptr of a tensor of this shape on the current device, 16-byte aligned
+    (int32 tensors: the prompts' bounds and the error word, 4-byte)."""
+    p = _ptr(t, dtype, name)
+    if p is None:
+        return None
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    if t.data_ptr() % (4 if t.dtype == torch.int32 else 16):
+        raise ValueError(f"{name} is not 16-byte aligned")
+    return p
 
 
 def _stream(stream=None):
@@ -259,6 +276,37 @@ def rssm_prefill(state, x, B, dt, A, stream=None):
     _check(lib().rssm_prefill(ct.byref(d), ct.byref(state.struct), T0, _ptr(x, in_dt, "x"), _ptr(B, in_dt, "B"),
                               _ptr(dt, torch.float32, "dt"), _ptr(A, torch.float32, "A"), _stream(stream)),
            "rssm_prefill")
+
+
+def rssm_prefill_scan_workspace_bytes(desc, total, max_seqlen):
+    return lib().rssm_prefill_scan_workspace_bytes(ct.byref(desc), int(total), int(max_seqlen))
+
+
+def rssm_prefill_scan(state, cu_seqlens, max_seqlen, x, B, C, dt, A, D, y, workspace=None, stream=None):
+    """The selective scan of packed prompts with their outputs, from and into
+    the fp32 checkpoint (pos must be 0): request b's tokens are rows
+    cu_seqlens[b] .. cu_seqlens[b+1]-1 of x, B, C, dt and y. workspace: a uint8
+    tensor of rssm_prefill_scan_workspace_bytes(desc, total, max_seqlen), or
+    None to allocate it for the call."""
+    d = state.desc
+    in_dt, f32 = _IN_DT[d.in_dtype], torch.float32
+    total, H, P, N, G = int(x.shape[0]), d.nheads, d.head_dim, d.d_state, d.ngroups
+    args = [_arg(cu_seqlens, torch.int32, (d.batch + 1,), "cu_seqlens"), _arg(x, in_dt, (total, H, P), "x"),
+            _arg(B, in_dt, (total, G, N), "B"), _arg(C, in_dt, (total, G, N), "C"), _arg(dt, f32, (total, H), "dt"),
+            _arg(A, f32, (H,), "A"), _arg(D, f32, (H,), "D"), _arg(y, f32, (total, H, P), "y")]
+    if state.pos.device != x.device:
+        raise ValueError(f"the state is on {state.pos.device}, x on {x.device}")
+    if workspace is None:
+        need = rssm_prefill_scan_workspace_bytes(d, total, max_seqlen)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+            if stream is not None:
+                workspace.record_stream(stream)
+    size = 0 if workspace is None else workspace.numel()
+    ws = _arg(workspace, torch.uint8, (size,), "workspace")
+    _check(lib().rssm_prefill_scan(ct.byref(d), ct.byref(state.struct), total, int(max_seqlen), *args, ws, size,
+                                   _stream(stream)), "rssm_prefill_scan")
+    return y
 
 
 def rssm_conv_step(desc, h, x, B, C, dt, A, D, y, stream=None):

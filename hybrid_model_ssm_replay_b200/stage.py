@@ -23,6 +23,11 @@ The projections and the attention are library calls; the SSM step and the
 block's element-wise glue run in librssm's kernels. scheme="replay" uses the
 replay decode (flush every interval tokens); scheme="conventional" the
 per-token read + write kernel on the same inputs and weights.
+
+HybridStage.prefill runs a prompt through the same blocks at once (replay
+scheme): the prompt forms of the block's steps, rssm_stage_conv_prompt,
+rssm_prefill_scan, rssm_stage_gate_norm_prompt and rssm_stage_add_norm, between
+the same GEMMs, and attention over the cache with the prompt's own tokens.
 """
 import ctypes as ct
 import math
@@ -67,6 +72,13 @@ def _lib():
         L.rssm_stage_conv.restype = ct.c_int
         L.rssm_stage_gate_norm.argtypes = [D, vp, vp, vp, ct.c_float, vp, vp]
         L.rssm_stage_gate_norm.restype = ct.c_int
+        i32, f32 = ct.c_int32, ct.c_float
+        L.rssm_stage_conv_prompt.argtypes = [D, i32] + [vp] * 12
+        L.rssm_stage_conv_prompt.restype = ct.c_int
+        L.rssm_stage_gate_norm_prompt.argtypes = [D, i32, vp, vp, vp, f32, vp, vp]
+        L.rssm_stage_gate_norm_prompt.restype = ct.c_int
+        L.rssm_stage_add_norm.argtypes = [i32, i32, i32, vp, vp, vp, vp, f32, vp, f32, vp, vp, vp]
+        L.rssm_stage_add_norm.restype = ct.c_int
         L._stage_sigs = True
     return L
 
@@ -88,6 +100,53 @@ def rssm_stage_gate_norm(desc, y, zxbcdt, norm_w, eps, out, stream=None):
                                             p(norm_w, torch.float32, "norm_w"), float(eps),
                                             p(out, torch.bfloat16, "out"), rssm._stream(stream)),
                 "rssm_stage_gate_norm")
+
+
+def rssm_stage_conv_prompt(desc, cu_seqlens, zxbcdt, conv_state, conv_w, conv_b, dt_bias, x, B, C, dt, err=None,
+                           stream=None):
+    """rssm_stage_conv for every token of packed prompts; conv_state is read
+    and updated. err: the state's error word (RssmState.err), or None."""
+    a, bf, f32 = rssm._arg, torch.bfloat16, torch.float32
+    H, P, N, G = desc.nheads, desc.head_dim, desc.d_state, desc.ngroups
+    total, chans = int(zxbcdt.shape[0]), H * P + 2 * G * N
+    rssm._check(_lib().rssm_stage_conv_prompt(
+        ct.byref(desc), total, a(cu_seqlens, torch.int32, (desc.batch + 1,), "cu_seqlens"),
+        a(zxbcdt, bf, (total, H * P + chans + H), "zxbcdt"), a(conv_state, bf, (desc.batch, 3, chans), "conv_state"),
+        a(conv_w, f32, (chans, 4), "conv_w"), a(conv_b, f32, (chans,), "conv_b"), a(dt_bias, f32, (H,), "dt_bias"),
+        a(x, bf, (total, H, P), "x"), a(B, bf, (total, G, N), "B"), a(C, bf, (total, G, N), "C"),
+        a(dt, f32, (total, H), "dt"), a(err, torch.int32, (1,), "err"), rssm._stream(stream)),
+        "rssm_stage_conv_prompt")
+
+
+def rssm_stage_gate_norm_prompt(desc, y, zxbcdt, norm_w, eps, out, stream=None):
+    """rssm_stage_gate_norm for every row of packed prompts (desc's batch is not used)."""
+    a, bf, f32 = rssm._arg, torch.bfloat16, torch.float32
+    H, P = desc.nheads, desc.head_dim
+    rows, din = int(zxbcdt.shape[0]), H * P
+    if tuple(y.shape) != (rows, din):
+        y = y.reshape(-1, din) if y.is_contiguous() and y.dim() == 3 and y.shape[1:] == (H, P) else y
+    rssm._check(_lib().rssm_stage_gate_norm_prompt(
+        ct.byref(desc), rows, a(y, f32, (rows, din), "y"),
+        a(zxbcdt, bf, (rows, 2 * din + 2 * desc.ngroups * desc.d_state + H), "zxbcdt"),
+        a(norm_w, f32, (din,), "norm_w"), float(eps), a(out, bf, (rows, din), "out"), rssm._stream(stream)),
+        "rssm_stage_gate_norm_prompt")
+    return out
+
+
+def rssm_stage_add_norm(u, v, pre_w, eps, out, post_w=None, gate=None, scale=1.0, u_out=None, stream=None):
+    """u_out = u + scale * gate * norm(v, post_w); out = norm(u_out, pre_w).
+    u_out None: u itself is updated. v None: the norm of u alone (u_out then
+    receives a copy, if it is given). pre_w and out None: no norm."""
+    a, bf, f32 = rssm._arg, torch.bfloat16, torch.float32
+    rows, dim = (int(n) for n in u.shape)
+    dt = u.dtype if u.dtype in (bf, f32) else (bf, f32)
+    up = a(u, dt, (rows, dim), "u")
+    uo = (None if v is None else up) if u_out is None else a(u_out, dt, (rows, dim), "u_out")
+    rssm._check(_lib().rssm_stage_add_norm(
+        rows, dim, rssm.RSSM_F32 if u.dtype == f32 else rssm.RSSM_BF16, up, a(v, bf, (rows, dim), "v"),
+        a(post_w, f32, (dim,), "post_w"), a(gate, f32, (dim,), "gate"), float(scale), a(pre_w, f32, (dim,), "pre_w"),
+        float(eps), uo, a(out, bf, (rows, dim), "out"), rssm._stream(stream)), "rssm_stage_add_norm")
+    return out
 
 
 def rmsnorm(u, w, eps):
@@ -159,6 +218,7 @@ class HybridStage:
             vc = (torch.randn(s.batch, s.kv_heads, s.ctx, s.attn_head_dim, generator=g)).to(torch.bfloat16)
             self.kv.append({"k": kc.to(device), "v": vc.to(device)})
         self.t = 0
+        self.t0 = 0  # the token from which the replay intervals count
         B_, din, gn = s.batch, s.d_inner, s.ngroups * s.d_state
         self.zx = torch.empty(B_, s.d_proj, dtype=torch.bfloat16, device=device)
         self.x = torch.empty(B_, s.nheads, s.head_dim, dtype=torch.bfloat16, device=device)
@@ -176,7 +236,7 @@ class HybridStage:
                         self.x, self.Bv, self.Cv, self.dt)
         if self.scheme == "replay":
             rssm.rssm_decode_step(st["state"], self.x, self.Bv, self.Cv, self.dt, b["A"], b["D"], self.y)
-            if (self.t + 1) % s.interval == 0:
+            if (self.t + 1 - self.t0) % s.interval == 0:
                 rssm.rssm_flush(st["state"], b["A"])
         else:
             rssm.rssm_conv_step(self.desc, st["state"], self.x, self.Bv, self.Cv, self.dt, b["A"], b["D"], self.y)
@@ -204,3 +264,70 @@ class HybridStage:
             u = self.attn_block(i, u)
         self.t += 1
         return u
+
+    def prefill(self, u):
+        """T prompt tokens per request at once: u [batch][T][d_model] bf16 ->
+        the residual stream after the stage, of every token. The same tokens
+        through step(), one by one, give the same up to rounding; step() goes
+        on from here. Replay scheme; T at most ctx when there is attention."""
+        s = self.shape
+        if self.scheme != "replay":
+            raise ValueError("prefill needs the replay scheme (a checkpoint to scan into)")
+        if u.dim() != 3 or u.shape[0] != s.batch or u.shape[2] != s.d_model or u.dtype != torch.bfloat16:
+            raise ValueError(f"u must be bf16 [{s.batch}][T][{s.d_model}]")
+        T = int(u.shape[1])
+        if s.n_attn and T > s.ctx:
+            raise ValueError(f"a prompt of {T} tokens does not fit the attention cache of {s.ctx}")
+        if T == 0:
+            return u.clone()
+        if (self.t - self.t0) % s.interval:  # decoded tokens still in the buffers
+            for b, st in zip(self.blocks, self.ssm):
+                rssm.rssm_flush(st["state"], b["A"], force=True)
+        rows, dev = s.batch * T, u.device
+        u = u.reshape(rows, s.d_model).clone()
+        cu = torch.arange(s.batch + 1, dtype=torch.int32, device=dev) * T
+        kw = dict(dtype=torch.bfloat16, device=dev)
+        n = torch.empty(rows, s.d_model, **kw)
+        zx = torch.empty(rows, s.d_proj, **kw)
+        x = torch.empty(rows, s.nheads, s.head_dim, **kw)
+        Bv = torch.empty(rows, s.ngroups, s.d_state, **kw)
+        Cv = torch.empty_like(Bv)
+        dt = torch.empty(rows, s.nheads, device=dev)
+        y = torch.empty(rows, s.nheads, s.head_dim, device=dev)
+        v = torch.empty(rows, s.d_inner, **kw)
+        norms = [b["norm"] for b in self.blocks] + [a["norm"] for a in self.attn] + [None]
+        if norms[0] is not None:
+            rssm_stage_add_norm(u, None, norms[0], s.eps, n)
+        for i, b in enumerate(self.blocks):
+            st = self.ssm[i]
+            torch.matmul(n, b["w_in"], out=zx)
+            rssm_stage_conv_prompt(self.desc, cu, zx, st["conv"], b["conv_w"], b["conv_b"], b["dt_bias"], x, Bv, Cv,
+                                   dt, err=st["state"].err)
+            rssm.rssm_prefill_scan(st["state"], cu, T, x, Bv, Cv, dt, b["A"], b["D"], y)
+            rssm_stage_gate_norm_prompt(self.desc, y, zx, b["gnorm"], s.eps, v)
+            nxt = norms[i + 1]
+            rssm_stage_add_norm(u, torch.matmul(v, b["w_out"]), nxt, s.eps, None if nxt is None else n)
+        for i in range(s.n_attn):
+            nxt = norms[s.n_ssm + i + 1]
+            rssm_stage_add_norm(u, self._attn_prompt(i, n, T), nxt, s.eps, None if nxt is None else n)
+        self.t += T
+        self.t0 = self.t
+        return u.view(s.batch, T, s.d_model)
+
+    def _attn_prompt(self, i, n, T):
+        """An attention block's output for T tokens per request: token j sees
+        the prompt's tokens up to itself and the cache slots that none of
+        them has overwritten."""
+        s, a, kv = self.shape, self.attn[i], self.kv[i]
+        hq, hk, hd = s.attn_heads, s.kv_heads, s.attn_head_dim
+        qkv = torch.matmul(n, a["w_qkv"]).view(s.batch, T, hq + 2 * hk, hd).transpose(1, 2)
+        q, k, v = qkv[:, :hq], qkv[:, hq:hq + hk], qkv[:, hq + hk:]
+        j = torch.arange(T, device=n.device)
+        age = (torch.arange(s.ctx, device=n.device) - self.t) % s.ctx  # the token that overwrites the slot
+        seen = torch.cat([age[None, :] > j[:, None], j[None, :] <= j[:, None]], 1)
+        o = torch.nn.functional.scaled_dot_product_attention(
+            q, torch.cat([kv["k"], k], 2), torch.cat([kv["v"], v], 2), attn_mask=seen, enable_gqa=True)
+        slots = (self.t + j) % s.ctx
+        kv["k"][:, :, slots] = k
+        kv["v"][:, :, slots] = v
+        return torch.matmul(o.transpose(1, 2).reshape(s.batch * T, hq * hd), a["w_o"])

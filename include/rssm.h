@@ -81,7 +81,9 @@ enum {
     RSSM_DEVERR_POS_RANGE = 1,    /* pos[b] < 0 or > capacity */
     RSSM_DEVERR_CAPACITY = 2,     /* pos[b] + tokens > capacity */
     RSSM_DEVERR_ACCEPT_RANGE = 3, /* accepted count outside 0..K */
-    RSSM_DEVERR_TIMEOUT = 4       /* a bulk copy did not complete within its bound */
+    RSSM_DEVERR_TIMEOUT = 4,      /* a bulk copy did not complete within its bound */
+    RSSM_DEVERR_SEQ_RANGE = 5     /* packed prompts: cu_seqlens decreases, leaves 0..total or
+                                     holds a prompt longer than max_seqlen */
 };
 
 /* desc.flags */
@@ -281,6 +283,47 @@ RSSM_API rssm_status_t rssm_lowprec_refresh(const rssm_desc_t *desc, const rssm_
 RSSM_API rssm_status_t rssm_prefill(const rssm_desc_t *desc, const rssm_state_t *state, int32_t T0,
                                     const void *x, const void *B, const float *dt, const float *A,
                                     void *stream);
+
+/* Packed prompts (rssm_prefill_scan and the prompt calls of rssm_stage.h):
+ * the tokens of all requests lie back to back, request b's at rows
+ * cu_seqlens[b] .. cu_seqlens[b+1]-1 of every per-token array; cu_seqlens is
+ * a device int32 [batch+1], not decreasing, within 0..total. A request may
+ * have no tokens. Rows of no request (before cu_seqlens[0], from
+ * cu_seqlens[batch] on) are neither read nor written. */
+
+/* Selective scan of packed prompts with their outputs -- the prefill of a
+ * layer whose outputs the next layer needs (the article is silent on it):
+ * for every request, from its checkpoint,
+ *     h_t = exp(dt_t A) h_{t-1} + dt_t x_t B_t^T,   y_t = h_t C_t + D x_t
+ * over its tokens in order; the checkpoint ends as the state after the last
+ * one (zero it first for a fresh request), pos stays 0 and flush_count is
+ * unchanged, so decoding goes on from there. A request without tokens keeps
+ * its checkpoint.
+ *   x [total][H][P], B and C [total][G][N] (in_dtype); dt [total][H] float
+ *   (softplus-ed); A, D [H] float; y [total][H][P] float.
+ *   max_seqlen  a bound on the requests' lengths, known to the host; how long
+ *               prompts are split goes by it
+ *   workspace   rssm_prefill_scan_workspace_bytes(desc, total, max_seqlen)
+ *               bytes of device memory, 16-byte aligned, used by this call
+ *               alone until it has run; NULL where that is 0
+ * A long prompt of few requests is cut into segments that run at once: their
+ * states from zero, then the states joined in order, then the outputs from
+ * the joined states. Sums and the carried state are fp32.
+ * A NaN or infinity in the inputs of a token reaches that token and later
+ * ones of its request (of x: in its head_dim column), none before it.
+ * Requires an fp32 state (update_dtype F32, no output copy), else
+ * RSSM_ERR_UNSUPPORTED; total, max_seqlen >= 0. A workspace too small:
+ * RSSM_ERR_CAPACITY. Device errors: pos[b] != 0; a bad cu_seqlens range or a
+ * prompt longer than max_seqlen. That request is left untouched. */
+RSSM_API rssm_status_t rssm_prefill_scan(const rssm_desc_t *desc, const rssm_state_t *state, int32_t total,
+                                         int32_t max_seqlen, const int32_t *cu_seqlens, const void *x,
+                                         const void *B, const void *C, const float *dt, const float *A,
+                                         const float *D, float *y, void *workspace, size_t workspace_bytes,
+                                         void *stream);
+
+/* Bytes of workspace of rssm_prefill_scan for these sizes; 0 when it needs
+ * none or the description is invalid. Host-only. */
+RSSM_API size_t rssm_prefill_scan_workspace_bytes(const rssm_desc_t *desc, int32_t total, int32_t max_seqlen);
 
 /* Conventional decode step, the in-run comparison (s1: read and write the
  * whole state every token): h <- a h + dt x B^T; y = h C + D x.

@@ -1,7 +1,7 @@
 /*
- * rssm_stage.h -- C ABI of the two element-wise steps of a Mamba-2 mixer
- * block that sit around the replay SSM step in a hybrid SSM/attention
- * decode stage (librssm.so).
+ * rssm_stage.h -- C ABI of the element-wise steps of a Mamba-2 mixer block
+ * that sit around the SSM step in a hybrid SSM/attention stage, for single
+ * tokens and for packed prompts (librssm.so).
  *
  * The ReplaySSM article (devotd.net "nvidia-replayssm-hybrid-model-ssm-
  * decoding-state-buffer", s2 "Reduce state transfers at large batch sizes")
@@ -63,6 +63,51 @@ RSSM_API rssm_status_t rssm_stage_conv(const rssm_desc_t *desc, const void *zxbc
  * Requires in_dtype BF16 and d_inner / G a multiple of 4. */
 RSSM_API rssm_status_t rssm_stage_gate_norm(const rssm_desc_t *desc, const float *y, const void *zxbcdt,
                                             const float *norm_w, float eps, void *out, void *stream);
+
+/* rssm_stage_conv over packed prompts (rssm.h, "Packed prompts"): the same
+ * conv, SiLU and softplus for every token of every request, the three inputs
+ * before a request's first token taken from its conv state; the conv state
+ * ends as the request's last three inputs (of a prompt shorter than three,
+ * after what is left of the old state), so decoding goes on from there. Each
+ * token's results are those of rssm_stage_conv, bit for bit.
+ *   zxbcdt  bf16 [total][Dp] (read only); cu_seqlens device int32 [batch+1]
+ *   x [total][H][P], B and C [total][G][N] bf16; dt [total][H] float
+ *   conv_state, conv_w, conv_b, dt_bias as in rssm_stage_conv
+ *   err     device int32, the error word (state->err), or NULL
+ * total >= 0. Device error: a bad cu_seqlens range (RSSM_DEVERR_SEQ_RANGE;
+ * that request is left untouched). */
+RSSM_API rssm_status_t rssm_stage_conv_prompt(const rssm_desc_t *desc, int32_t total, const int32_t *cu_seqlens,
+                                              const void *zxbcdt, void *conv_state, const float *conv_w,
+                                              const float *conv_b, const float *dt_bias, void *x, void *B,
+                                              void *C, float *dt, int32_t *err, void *stream);
+
+/* rssm_stage_gate_norm over the rows of packed prompts: the same formula for
+ * `rows` rows (desc's batch is not used), any number of them, and any group
+ * size d_inner / G.
+ *   y float [rows][d_inner]; zxbcdt bf16 [rows][Dp]; norm_w float [d_inner];
+ *   out bf16 [rows][d_inner]; eps > 0; rows >= 0. */
+RSSM_API rssm_status_t rssm_stage_gate_norm_prompt(const rssm_desc_t *desc, int32_t rows, const float *y,
+                                                   const void *zxbcdt, const float *norm_w, float eps,
+                                                   void *out, void *stream);
+
+/* Between two blocks, for every row of width dim: the norm after the block,
+ * its gate and residual scale, the residual add, and the norm before the
+ * next block,
+ *   v' = v / sqrt(mean(v^2) + eps) * post_w      (v itself without post_w)
+ *   u' = u + scale * gate * v'                   (rounded to the stream's type)
+ *   out = u' / sqrt(mean(u'^2) + eps) * pre_w    (of the rounded u').
+ *   u       stream [rows][dim], u_dtype RSSM_F32 or RSSM_BF16
+ *   v       bf16 [rows][dim]: the block's output (its last projection), or
+ *           NULL: u' = u (post_w and gate are then not used)
+ *   post_w, gate  float [dim] or NULL
+ *   pre_w, out    float [dim], bf16 [rows][dim]; both NULL: no norm before
+ *   u_out   stream [rows][dim]; u itself is allowed. With v NULL it may be
+ *           NULL (nothing to store)
+ * No other overlap of arguments is allowed. eps > 0; scale finite; rows >= 0;
+ * 1 <= dim <= 16384, else RSSM_ERR_SHAPE. Sums are fp32. */
+RSSM_API rssm_status_t rssm_stage_add_norm(int32_t rows, int32_t dim, int32_t u_dtype, const void *u,
+                                           const void *v, const float *post_w, const float *gate, float scale,
+                                           const float *pre_w, float eps, void *u_out, void *out, void *stream);
 
 #ifdef __cplusplus
 }
