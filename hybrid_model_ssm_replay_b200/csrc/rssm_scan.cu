@@ -186,6 +186,532 @@ __global__ void __launch_bounds__(kThreads) k_scan(const ScanArgs a) {
 }
 
 // ---------------------------------------------------------------------------
+// k_scan_umma: the scan in blocks of 128 tokens on the 5th-generation tensor
+// cores (bf16 inputs, head_dim a multiple of 8). With c_t the log decay from
+// the block's start through token t and h the state before the block,
+//     y_t  = exp(c_t) C_t h^T + sum_{s <= t} M_ts x_s + D x_t,
+//     M_ts = (C_t . B_s) exp(c_t - c_s) dt_s,
+//     h   <- exp(c_127) h + sum_s w_s x_s B_s^T,   w_s = dt_s exp(c_127 - c_s),
+// four products with K = 128 or d_state. One CTA of 256 threads per (item,
+// head, 64 columns of its head_dim), two CTAs per SM; per block:
+//   S = C B^T          [128 t x 128 s], C and B as loaded (exact bf16);
+//   O = C [h_hi|h_lo]  [128 t x 128], the state in two bf16 parts;
+//   Y = M x            [128 t x 64], M in three parts, built in tensor memory
+//                      over S by the threads that own its rows, x as loaded;
+//   U = B^T [w x]      [128 n x 192], w x in three parts.
+// Thread (warp w, lane l) owns token and state row 32 (w % 4) + l and half
+// the columns (w / 4). The state stays in fp32 registers; O is read, scaled
+// and kept in registers before M's third part takes its place in tensor
+// memory; U takes M's. 112 KB of shared memory: C, B, x, and one buffer that
+// holds the parts of h and then, with half of C's (read by then), of w x.
+//
+// Decays. No difference of two long sums is formed: within a 32-token block
+// the exponent of M is a running sum of dt from s + 1 to t, and across
+// blocks M's factor is (start of t's block .. t) x (blocks between) x (s + 1
+// .. end of s's block), each the exponential of a sum of positive terms.
+//
+// Precision: a product of bf16 factors is exact in the fp32 sum. In two
+// parts everywhere, an output of a 512-token prompt was 1e-4 of the rms off
+// at worst and 2.3e-6 in the 2-norm; three parts (2^-26) of M and w x and
+// two (2^-18) of the state, which the next block reads from fp32 again,
+// give 3e-7.
+//
+// x is the one raw operand of Y, so M's zeros (s > t) meet every x of the
+// block. In a block with a NaN or infinity in x, Y is formed with zeros in
+// their place and they are added for t >= s on the CUDA cores, so that no
+// output before them changes.
+// ---------------------------------------------------------------------------
+constexpr int kSuTok = 128;                    // tokens per block
+constexpr uint32_t kSuBlk = kSuTok * 128u;     // 128 rows of 128 bytes, swizzled: 16 KB
+constexpr uint32_t kSuB = 0;                   // B rows, two 64-column blocks
+constexpr uint32_t kSuX = 2 * kSuBlk;          // x rows
+constexpr uint32_t kSuR = 3 * kSuBlk;          // parts of h (2) or w x (hi, mid)
+constexpr uint32_t kSuC1 = 5 * kSuBlk;         // C columns 64.. ; later w x lo (right behind hi, mid)
+constexpr uint32_t kSuC0 = 6 * kSuBlk;         // C columns 0..63
+constexpr uint32_t kSuCol = 7 * kSuBlk;        // float [128]: dt_s exp(decay from s + 1 to its 32-block's end)
+constexpr uint32_t kSuSum = kSuCol + 512;      // float [4]: dt sums of the 32-blocks
+constexpr uint32_t kSuBar = kSuSum + 16;       // 3 mbarriers, tensor-memory address
+constexpr uint32_t kSuSmem = kSuBar + 32;
+constexpr uint32_t kSuCols = 256;              // tensor-memory columns
+constexpr uint32_t kTmS = 0, kTmLo = 128, kTmY = 192;  // S / M hi, mid; M lo; Y (O: 128..255, U: 0..191)
+
+// Shared-memory matrix descriptor of a 128-byte-swizzled operand: start
+// address, leading and stride byte offsets in 16-byte units, version 1.
+__device__ __forceinline__ uint64_t su_desc(uint32_t addr) {
+    return static_cast<uint64_t>((addr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(kSuBlk >> 4) << 16) |
+           (static_cast<uint64_t>(1024u >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+
+// Instruction descriptor: fp32 accumulator, bf16 A and B, M = 128.
+__host__ __device__ constexpr uint32_t su_idesc(uint32_t n, uint32_t a_mn, uint32_t b_mn) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | (a_mn << 15) | (b_mn << 16) | ((n >> 3) << 17) | ((128u >> 4) << 24);
+}
+
+template <uint32_t IDESC>
+__device__ __forceinline__ void su_mma(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, {%5, %5, %5, %5}, p;\n\t}" ::"r"(d),
+        "l"(adesc), "l"(bdesc), "r"(IDESC), "r"(accumulate), "r"(0u)
+        : "memory");
+}
+
+// The A operand from tensor memory.
+template <uint32_t IDESC>
+__device__ __forceinline__ void su_mma_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, {%5, %5, %5, %5}, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(bdesc), "r"(IDESC), "r"(accumulate), "r"(0u)
+        : "memory");
+}
+
+__device__ __forceinline__ void su_commit(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void su_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void su_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void su_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void su_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// 16 / 8 consecutive 32-bit columns of this thread's row. The values may be
+// used after su_wait_ld only.
+__device__ __forceinline__ void su_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void su_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+}
+__device__ __forceinline__ void su_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(taddr)
+                 : "memory");
+}
+
+__device__ __forceinline__ float su_exp2(float v) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    uint32_t d;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+
+// A pair of bf16 with zeros in the place of NaN and infinities.
+__device__ __forceinline__ uint32_t finite2(uint32_t w) {
+    const uint32_t lo = (w & 0x7F80u) == 0x7F80u ? 0u : w & 0xFFFFu;
+    return lo | ((w & 0x7F800000u) == 0x7F800000u ? 0u : w & 0xFFFF0000u);
+}
+
+// Two fp32 values as bf16 pairs hi + mid + lo (each the nearest bf16 of what
+// the parts before leave; the differences are exact).
+__device__ __forceinline__ void split3(float v0, float v1, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
+    hi = pack_bf16(v0, v1);
+    const float r0 = v0 - bf_lo(hi), r1 = v1 - bf_hi(hi);
+    mid = pack_bf16(r0, r1);
+    lo = pack_bf16(r0 - bf_lo(mid), r1 - bf_hi(mid));
+}
+
+__device__ __forceinline__ void su_cp16(uint32_t dst, const void* src, bool valid) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16u : 0u)
+                 : "memory");
+}
+
+template <bool OUT>
+__global__ void __launch_bounds__(256, 2) k_scan_umma(const ScanArgs a, const int slices) {
+    extern __shared__ __align__(1024) unsigned char smem[];
+    const int H = a.s.H, P = a.s.P, N = a.s.N, G = a.s.G;
+    const int hs = blockIdx.x % (H * slices), h = hs / slices, p0 = 64 * (hs - h * slices);
+    Item it;
+    if (!find_item<OUT>(a, blockIdx.x / (H * slices), it)) return;
+    const int g = h / (H / G), tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int q = warp & 3, half = warp >> 2;  // rows 32 q .., columns of half `half`
+    const int row = 32 * q + lane;             // this thread's token and state row
+    const uint32_t sb = smem_u32(smem);
+    if (sb & 1023u) {  // the swizzled operands lie on 1024-byte boundaries
+        if (tid == 0) set_error(a.err, RSSM_DEVERR_TIMEOUT);
+        return;
+    }
+    const uint32_t bar_o = sb + kSuBar, bar_y = bar_o + 8, bar_u = bar_o + 16;
+    float* s_col = reinterpret_cast<float*>(smem + kSuCol);
+    float* s_sum = reinterpret_cast<float*>(smem + kSuSum);
+    if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sb + kSuBar + 24),
+                     "r"(kSuCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    if (tid == 0) {
+        mbar_init(bar_o, 1);
+        mbar_init(bar_y, 1);
+        mbar_init(bar_u, 1);
+    }
+
+    const __nv_bfloat16* xg = static_cast<const __nv_bfloat16*>(a.x) + static_cast<size_t>(h) * P + p0;
+    const __nv_bfloat16* Bg = static_cast<const __nv_bfloat16*>(a.B) + static_cast<size_t>(g) * N;
+    const __nv_bfloat16* Cg = static_cast<const __nv_bfloat16*>(a.C) + static_cast<size_t>(g) * N;
+    const size_t xstep = static_cast<size_t>(H) * P, bstep = static_cast<size_t>(G) * N;
+    // 64 columns from c0 of 128 token rows (tokens t0 ..) into the buffer at
+    // `buf`: row k's 16-byte chunk j at chunk j ^ (k & 7); zeros past the
+    // item's tokens and past column `cols`
+    auto fetch = [&](uint32_t buf, const __nv_bfloat16* src, size_t step, int t0, int c0, int cols) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int k = (tid >> 3) + 32 * i, j = tid & 7;
+            const bool ok = t0 + k < it.t1 && c0 + 8 * j < cols;
+            su_cp16(sb + buf + k * 128 + 16 * (j ^ (k & 7)), ok ? src + (t0 + k) * step + c0 + 8 * j : src, ok);
+        }
+    };
+    auto fetch_B = [&](int t0) {
+        fetch(kSuB, Bg, bstep, t0, 0, N);
+        if (N > 64) fetch(kSuB + kSuBlk, Bg, bstep, t0, 64, N);
+    };
+    const float* dtg = a.dt + h;
+    auto load_dt = [&](int t0) { return t0 + row < it.t1 ? dtg[static_cast<size_t>(t0 + row) * H] : 0.f; };
+
+    fetch_B(it.t0);
+    fetch(kSuX, xg, xstep, it.t0, 0, P - p0);
+    if (OUT) {
+        fetch(kSuC0, Cg, bstep, it.t0, 0, N);
+        if (N > 64) fetch(kSuC1, Cg, bstep, it.t0, 64, N);
+    }
+    float dt = load_dt(it.t0);
+    const float A2 = a.A[h] * 1.4426950408889634f;  // decays as powers of two
+    const float Dh = OUT ? a.D[h] : 0.f;
+
+    // the state: row `row` (d_state), columns 32 half .. + 31 of the head_dim slice
+    float hst[32];
+    const float* init = it.slot < 0 ? head_state(a, it.b, h) : slot_state(a, it.slot, h);
+    const int pb = p0 + 32 * half;  // this thread's first column
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+        hst[j] = OUT && row < N && pb + j < P ? init[static_cast<size_t>(pb + j) * N + row] : 0.f;
+
+    // 16-byte chunk j of this thread's row in a buffer
+    auto chunk = [&](uint32_t buf, int j) {
+        return reinterpret_cast<uint4*>(smem + buf + row * 128 + 16 * (j ^ (row & 7)));
+    };
+    auto put_state = [&]() {  // hi and lo parts of the state, d_state row by row
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float v0 = hst[8 * j + 2 * i], v1 = hst[8 * j + 2 * i + 1];
+                hi[i] = pack_bf16(v0, v1);
+                lo[i] = pack_bf16(v0 - bf_lo(hi[i]), v1 - bf_hi(hi[i]));
+            }
+            *chunk(kSuR, 4 * half + j) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *chunk(kSuR + kSuBlk, 4 * half + j) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
+    };
+    if (OUT) put_state();
+    su_fence_before();
+    __syncthreads();
+    su_fence_after();
+    const uint32_t tm = *reinterpret_cast<volatile uint32_t*>(smem + kSuBar + 24);
+    const uint32_t tml = tm + (static_cast<uint32_t>(32 * q) << 16);  // this warp's lanes
+    float dtsum = 0.f;
+    bool timed_out = false;
+
+    int par = 0;
+    for (int t0 = it.t0; t0 < it.t1; t0 += kSuTok, par ^= 1) {
+        const bool more = t0 + kSuTok < it.t1;
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        su_fence_before();
+        __syncthreads();  // the block and the state's parts are in place
+        su_fence_after();
+        if (OUT && tid == 0) {
+            for (int ks = 0; ks < N / 16; ++ks) {
+                const uint32_t kc = (ks < 4 ? kSuC0 : kSuC1) + 32 * (ks & 3);
+                const uint32_t kb = kSuB + (ks < 4 ? 0u : kSuBlk) + 32 * (ks & 3);
+                su_mma<su_idesc(128, 0, 0)>(tm + kTmS, su_desc(sb + kc), su_desc(sb + kb), ks > 0);
+            }
+            for (int ks = 0; ks < N / 16; ++ks) {
+                const uint32_t kc = (ks < 4 ? kSuC0 : kSuC1) + 32 * (ks & 3);
+                su_mma<su_idesc(128, 0, 1)>(tm + kTmLo, su_desc(sb + kc), su_desc(sb + kSuR + 2048 * ks), ks > 0);
+            }
+            su_commit(bar_o);
+        }
+        // decays of this thread's token within its 32-block
+        const float d = dt;
+        if (more) dt = load_dt(t0 + kSuTok);
+        float pre = d, suf = d;  // inclusive sums from the block's start, to its end
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const float u = __shfl_up_sync(0xffffffffu, pre, off), v = __shfl_down_sync(0xffffffffu, suf, off);
+            if (lane >= off) pre += u;
+            if (lane + off < 32) suf += v;
+        }
+        const float next = __shfl_down_sync(0xffffffffu, suf, 1);
+        const float col = d * su_exp2(A2 * (lane == 31 ? 0.f : next));
+        if (half == 0) {
+            s_col[row] = col;
+            if (lane == 0) s_sum[q] = suf;
+        }
+        bool bad = false;
+        if (OUT) {
+            const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
+            __nv_bfloat162 z = zero;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint4 u = *chunk(kSuX, 4 * half + j);
+                z = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&u.x), zero, z);
+                z = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&u.y), zero, z);
+                z = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&u.z), zero, z);
+                z = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&u.w), zero, z);
+            }
+            bad = __hisnan(z.x) || __hisnan(z.y);
+        }
+        bad = __syncthreads_or(bad);  // and s_col, s_sum are written
+        if (bad) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint4* c = chunk(kSuX, 4 * half + j);
+                const uint4 u = *c;
+                *c = make_uint4(finite2(u.x), finite2(u.y), finite2(u.z), finite2(u.w));
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        }
+        // chunk j of x of this block's token s, as given
+        auto x_given = [&](int s, int j) {
+            if (!bad) return *reinterpret_cast<const uint4*>(smem + kSuX + s * 128 + 16 * (j ^ (s & 7)));
+            if (t0 + s >= it.t1 || p0 + 8 * j >= P) return make_uint4(0, 0, 0, 0);
+            return *reinterpret_cast<const uint4*>(xg + (t0 + s) * xstep + 8 * j);
+        };
+        float before = 0.f, after = 0.f;  // dt sums of the 32-blocks before and after this one
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float s = s_sum[k];
+            before += k < q ? s : 0.f;
+            after += k > q ? s : 0.f;
+        }
+        const float total = s_sum[0] + s_sum[1] + s_sum[2] + s_sum[3];
+
+        float yo[32];
+        if (OUT) {
+            const float rowf = su_exp2(A2 * pre);
+            if (!mbar_wait_bounded(bar_o, par, kWaitNs)) timed_out = true;
+            su_fence_after();
+            // the state's share of the outputs, columns 32 half ..
+            const float fac = rowf * su_exp2(A2 * before);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                uint32_t hi[16], lo[16];
+                su_ld16(tml + kTmLo + 32 * half + 16 * j, hi);
+                su_ld16(tml + kTmY + 32 * half + 16 * j, lo);
+                su_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    yo[16 * j + i] = fac * (__uint_as_float(hi[i]) + __uint_as_float(lo[i]));
+            }
+            // M over S, 32-blocks 2 half and 2 half + 1 of its columns, 16 at a
+            // time: hi and mid parts in the columns read, lo in its own
+#pragma unroll
+            for (int jb = 1; jb >= 0; --jb) {
+                const int J = 2 * half + jb;
+                if (J > q) {  // nothing but later tokens
+                    const uint32_t zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        su_st8(tml + kTmS + 32 * J + 16 * k, zero);
+                        su_st8(tml + kTmS + 32 * J + 16 * k + 8, zero);
+                        su_st8(tml + kTmLo + 16 * J + 8 * k, zero);
+                    }
+                    continue;
+                }
+                float between = 0.f;
+#pragma unroll
+                for (int k = 1; k < 4; ++k) between += k > J && k < q ? s_sum[k] : 0.f;
+                const float rb = rowf * su_exp2(A2 * between);
+                float run = 0.f;  // dt sum from s + 1 to t
+#pragma unroll
+                for (int k = 1; k >= 0; --k) {
+                    uint32_t v[16];
+                    su_ld16(tml + kTmS + 32 * J + 16 * k, v);
+                    su_wait_ld();
+                    float m[16];
+                    if (J == q) {
+#pragma unroll
+                        for (int i = 15; i >= 0; --i) {
+                            const int s = 16 * k + i;
+                            if (s < 31) {
+                                const float dn = __shfl_sync(0xffffffffu, d, (s + 1) & 31);
+                                run += lane > s ? dn : 0.f;
+                            }
+                            const float ds = __shfl_sync(0xffffffffu, d, s);
+                            const float f = lane == s ? ds : ds * su_exp2(A2 * run);
+                            m[i] = lane >= s ? __uint_as_float(v[i]) * f : 0.f;
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 16; i += 4) {
+                            const float4 c4 = *reinterpret_cast<const float4*>(s_col + 32 * J + 16 * k + i);
+                            m[i] = __uint_as_float(v[i]) * (rb * c4.x);
+                            m[i + 1] = __uint_as_float(v[i + 1]) * (rb * c4.y);
+                            m[i + 2] = __uint_as_float(v[i + 2]) * (rb * c4.z);
+                            m[i + 3] = __uint_as_float(v[i + 3]) * (rb * c4.w);
+                        }
+                    }
+                    uint32_t hi[8], mid[8], lo[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) split3(m[2 * i], m[2 * i + 1], hi[i], mid[i], lo[i]);
+                    su_st8(tml + kTmS + 32 * J + 16 * k, hi);
+                    su_st8(tml + kTmS + 32 * J + 16 * k + 8, mid);
+                    su_st8(tml + kTmLo + 16 * J + 8 * k, lo);
+                }
+            }
+            su_wait_st();
+            su_fence_before();
+            __syncthreads();  // M is complete; C and the state's parts have been read
+            su_fence_after();
+            if (tid == 0) {
+                for (int ks = 0; ks < kSuTok / 16; ++ks) {
+                    const uint64_t xd = su_desc(sb + kSuX + 2048 * ks);
+                    su_mma_ts<su_idesc(64, 0, 1)>(tm + kTmY, tm + kTmS + 16 * ks, xd, ks > 0);
+                    su_mma_ts<su_idesc(64, 0, 1)>(tm + kTmY, tm + kTmS + 16 * ks + 8, xd, 1);
+                    su_mma_ts<su_idesc(64, 0, 1)>(tm + kTmY, tm + kTmLo + 8 * ks, xd, 1);
+                }
+                su_commit(bar_y);
+            }
+            if (more) fetch(kSuC0, Cg, bstep, t0 + kSuTok, 0, N);
+        }
+        // w x in three parts
+        {
+            const float w = col * su_exp2(A2 * after);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint4 u = x_given(row, 4 * half + j);
+                const uint32_t xu[4] = {u.x, u.y, u.z, u.w};
+                uint32_t hi[4], mid[4], lo[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) split3(w * bf_lo(xu[i]), w * bf_hi(xu[i]), hi[i], mid[i], lo[i]);
+                *chunk(kSuR, 4 * half + j) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                *chunk(kSuR + kSuBlk, 4 * half + j) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
+                *chunk(kSuC1, 4 * half + j) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            }
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        su_fence_before();
+        __syncthreads();
+        su_fence_after();
+        if (OUT && !mbar_wait_bounded(bar_y, par, kWaitNs)) timed_out = true;  // Y done, M read
+        su_fence_after();
+        if (OUT && bad) {  // what was left out of Y, 8 columns at a time, before U takes M's place
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll 1
+                for (int ks = 0; ks < kSuTok / 16; ++ks) {
+                    uint32_t hi[8], mid[8], lo[8];
+                    su_ld8(tml + kTmS + 16 * ks, hi);
+                    su_ld8(tml + kTmS + 16 * ks + 8, mid);
+                    su_ld8(tml + kTmLo + 8 * ks, lo);
+                    su_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const int s = 16 * ks + i;
+                        const float m = i & 1 ? bf_hi(hi[i / 2]) + (bf_hi(mid[i / 2]) + bf_hi(lo[i / 2]))
+                                              : bf_lo(hi[i / 2]) + (bf_lo(mid[i / 2]) + bf_lo(lo[i / 2]));
+                        const uint4 u = x_given(s, 4 * half + j);
+                        const uint32_t xu[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            const uint32_t out = finite2(xu[c]) ^ xu[c];
+                            if (s <= row && (out & 0xFFFFu)) acc[2 * c] = fmaf(m, bf_lo(xu[c]), acc[2 * c]);
+                            if (s <= row && (out >> 16)) acc[2 * c + 1] = fmaf(m, bf_hi(xu[c]), acc[2 * c + 1]);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) yo[8 * j + i] += acc[i];
+            }
+            su_fence_before();
+            __syncthreads();
+            su_fence_after();
+        }
+        if (tid == 0) {
+            for (int ks = 0; ks < kSuTok / 16; ++ks)
+                su_mma<su_idesc(192, 1, 1)>(tm + kTmS, su_desc(sb + kSuB + 2048 * ks), su_desc(sb + kSuR + 2048 * ks),
+                                            ks > 0);
+            su_commit(bar_u);
+        }
+        if (OUT) {
+            const int t = t0 + row;
+            float* yr = a.y + (static_cast<size_t>(t) * H + h) * P + pb;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint32_t v[8];
+                su_ld8(tml + kTmY + 32 * half + 8 * j, v);
+                su_wait_ld();
+                const uint4 u = x_given(row, 4 * half + j);
+                const float xv[8] = {bf_lo(u.x), bf_hi(u.x), bf_lo(u.y), bf_hi(u.y),
+                                     bf_lo(u.z), bf_hi(u.z), bf_lo(u.w), bf_hi(u.w)};
+                float o[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) o[i] = fmaf(Dh, xv[i], yo[8 * j + i]) + __uint_as_float(v[i]);
+                if (t < it.t1 && pb + 8 * j < P) {
+                    *reinterpret_cast<float4*>(yr + 8 * j) = make_float4(o[0], o[1], o[2], o[3]);
+                    *reinterpret_cast<float4*>(yr + 8 * j + 4) = make_float4(o[4], o[5], o[6], o[7]);
+                }
+            }
+        }
+        if (!mbar_wait_bounded(bar_u, par, kWaitNs)) timed_out = true;
+        su_fence_after();
+        __syncthreads();  // B, x and the parts of w x have been read
+        if (more) {
+            fetch_B(t0 + kSuTok);
+            fetch(kSuX, xg, xstep, t0 + kSuTok, 0, P - p0);
+            if (OUT && N > 64) fetch(kSuC1, Cg, bstep, t0 + kSuTok, 64, N);
+        }
+        const float dec = su_exp2(A2 * total);
+        dtsum += total;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            uint32_t u0[8], u1[8], u2[8];
+            su_ld8(tml + kTmS + 32 * half + 8 * j, u0);
+            su_ld8(tml + kTmS + 64 + 32 * half + 8 * j, u1);
+            su_ld8(tml + kTmS + 128 + 32 * half + 8 * j, u2);
+            su_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                hst[8 * j + i] = fmaf(dec, hst[8 * j + i],
+                                      __uint_as_float(u0[i]) + (__uint_as_float(u1[i]) + __uint_as_float(u2[i])));
+        }
+        if (OUT && more) put_state();
+    }
+    if (timed_out) set_error(a.err, RSSM_DEVERR_TIMEOUT);
+    if ((!OUT || it.last) && row < N) {
+        float* out = OUT ? head_state(a, it.b, h) : slot_state(a, it.slot, h);
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            if (pb + j < P) out[static_cast<size_t>(pb + j) * N + row] = hst[j];
+    }
+    if (!OUT && tid == 0 && p0 == 0) *slot_dtsum(a, it.slot, h) = dtsum;
+    su_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        su_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "r"(kSuCols) : "memory");
+    }
+}
+
+// ---------------------------------------------------------------------------
 // k_scan_join: the segments' start states, in place of their local states.
 // One thread per 4 state elements of a (request, head).
 // ---------------------------------------------------------------------------
@@ -212,8 +738,25 @@ __global__ void __launch_bounds__(kThreads) k_scan_join(const ScanArgs a) {
     }
 }
 
+// The tensor-core scan moves 16 bytes of an x row at a time.
+bool scan_umma_shape(const Shape& s, int in_bf16) {
+    return in_bf16 && s.P % 8 == 0 && static_cast<long long>(s.batch) * s.H * ((s.P + 63) / 64) <= 0x7fffffffLL;
+}
+
+template <bool OUT>
+cudaError_t launch_umma(const ScanArgs& a, int items, cudaStream_t st) {
+    const int slices = (a.s.P + 63) / 64;
+    cudaError_t e = cudaFuncSetAttribute(k_scan_umma<OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(kSuSmem));
+    if (e != cudaSuccess) return e;
+    const dim3 grid(static_cast<unsigned>(items) * static_cast<unsigned>(a.s.H) * static_cast<unsigned>(slices));
+    k_scan_umma<OUT><<<grid, 256, kSuSmem, st>>>(a, slices);
+    return cudaGetLastError();
+}
+
 template <typename TIn, bool OUT>
 cudaError_t launch_pass(const ScanArgs& a, int items, cudaStream_t st) {
+    if (scan_umma_shape(a.s, sizeof(TIn) == 2)) return launch_umma<OUT>(a, items, st);
     const size_t smem = 4u * kScanTok * (2 * static_cast<size_t>(a.s.P) + 2 * static_cast<size_t>(a.s.N));
     const int passes = (a.s.P * a.s.lpr + kThreads - 1) / kThreads;
     const dim3 grid(static_cast<unsigned>(items) * static_cast<unsigned>(a.s.H));
@@ -238,7 +781,7 @@ int scan_segment_len(const Shape& s, int in_bf16, int total, int max_seqlen) {
     const long long share = static_cast<long long>(total) * s.H / fill;  // tokens per CTA, evenly cut
     if (max_seqlen <= 256 || max_seqlen <= 2 * share) return 0;
     const long long len = share < 128 ? 128 : (share + 127) / 128 * 128;
-    if ((total / len + s.batch) * s.H > 0x7fffffffLL) return 0;  // one CTA per slot and head
+    if ((total / len + s.batch) * s.H * ((s.P + 63) / 64) > 0x7fffffffLL) return 0;  // one CTA per slot and head
     return static_cast<int>(len);
 }
 
