@@ -12,8 +12,11 @@
 // workspace slot floor(cu[b] / seg_len) + b + s: a request has at most
 // floor(cu[b+1] / seg_len) - floor(cu[b] / seg_len) + 1 segments, so slots
 // never meet, and there are at most floor(total / seg_len) + batch of them.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+
+#include <atomic>
 
 #include "rssm.h"
 #include "rssm_device.cuh"
@@ -195,15 +198,17 @@ __global__ void __launch_bounds__(kThreads) k_scan(const ScanArgs a) {
 // four products with K = 128 or d_state. One CTA of 256 threads per (item,
 // head, 64 columns of its head_dim), two CTAs per SM; per block:
 //   S = C B^T          [128 t x 128 s], C and B as loaded (exact bf16);
-//   O = C [h_hi|h_lo]  [128 t x 128], the state in two bf16 parts;
+//   O = C h^T          [128 t x 64], the state in two bf16 parts;
 //   Y = M x            [128 t x 64], M in three parts, built in tensor memory
 //                      over S by the threads that own its rows, x as loaded;
 //   U = B^T [w x]      [128 n x 192], w x in three parts.
 // Thread (warp w, lane l) owns token and state row 32 (w % 4) + l and half
-// the columns (w / 4). The state stays in fp32 registers; O is read, scaled
-// and kept in registers before M's third part takes its place in tensor
-// memory; U takes M's. 112 KB of shared memory: C, B, x, and one buffer that
-// holds the parts of h and then, with half of C's (read by then), of w x.
+// the columns (w / 4). The state stays in fp32 registers; O is read and
+// scaled, with D x added, before Y takes its place in tensor memory; U takes
+// M's. 112 KB of shared memory: C, B, x, and one buffer that holds the parts
+// of h and then, with half of C's (read by then), of w x. Each part of the
+// next block is fetched (TMA) as soon as its buffer has been read. Rows past
+// the request's end are zeroed in x and B.
 //
 // Decays. No difference of two long sums is formed: within a 32-token block
 // the exponent of M is a running sum of dt from s + 1 to t, and across
@@ -230,10 +235,10 @@ constexpr uint32_t kSuC1 = 5 * kSuBlk;         // C columns 64.. ; later w x lo 
 constexpr uint32_t kSuC0 = 6 * kSuBlk;         // C columns 0..63
 constexpr uint32_t kSuCol = 7 * kSuBlk;        // float [128]: dt_s exp(decay from s + 1 to its 32-block's end)
 constexpr uint32_t kSuSum = kSuCol + 512;      // float [4]: dt sums of the 32-blocks
-constexpr uint32_t kSuBar = kSuSum + 16;       // 3 mbarriers, tensor-memory address
-constexpr uint32_t kSuSmem = kSuBar + 32;
+constexpr uint32_t kSuBar = kSuSum + 16;       // 5 mbarriers, tensor-memory address
+constexpr uint32_t kSuSmem = kSuBar + 48;
 constexpr uint32_t kSuCols = 256;              // tensor-memory columns
-constexpr uint32_t kTmS = 0, kTmLo = 128, kTmY = 192;  // S / M hi, mid; M lo; Y (O: 128..255, U: 0..191)
+constexpr uint32_t kTmS = 0, kTmLo = 128, kTmY = 192;  // S, then M hi, mid; M lo; O, then Y (U: 0..191)
 
 // Shared-memory matrix descriptor of a 128-byte-swizzled operand: start
 // address, leading and stride byte offsets in 16-byte units, version 1.
@@ -305,11 +310,30 @@ __device__ __forceinline__ float su_exp2(float v) {
 
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+__device__ __forceinline__ float2 bf2(uint32_t w) { return make_float2(bf_lo(w), bf_hi(w)); }
+__device__ __forceinline__ uint32_t pack_bf16(float2 v) {
     uint32_t d;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(v.y), "f"(v.x));
     return d;
 }
+
+// Two fp32 lanes in one instruction.
+#define RSSM_F32X2(name, op)                                                       \
+    __device__ __forceinline__ float2 name(float2 a, float2 b) {                   \
+        float2 d;                                                                  \
+        asm("{\n\t.reg .b64 ra, rb, rd;\n\t"                                       \
+            "mov.b64 ra, {%2, %3};\n\t"                                            \
+            "mov.b64 rb, {%4, %5};\n\t" op                                         \
+            " rd, ra, rb;\n\t"                                                     \
+            "mov.b64 {%0, %1}, rd;\n\t}"                                           \
+            : "=f"(d.x), "=f"(d.y)                                                 \
+            : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));                             \
+        return d;                                                                  \
+    }
+RSSM_F32X2(add2, "add.rn.f32x2")
+RSSM_F32X2(sub2, "sub.rn.f32x2")
+RSSM_F32X2(mul2, "mul.rn.f32x2")
+#undef RSSM_F32X2
 
 // A pair of bf16 with zeros in the place of NaN and infinities.
 __device__ __forceinline__ uint32_t finite2(uint32_t w) {
@@ -319,20 +343,26 @@ __device__ __forceinline__ uint32_t finite2(uint32_t w) {
 
 // Two fp32 values as bf16 pairs hi + mid + lo (each the nearest bf16 of what
 // the parts before leave; the differences are exact).
-__device__ __forceinline__ void split3(float v0, float v1, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
-    hi = pack_bf16(v0, v1);
-    const float r0 = v0 - bf_lo(hi), r1 = v1 - bf_hi(hi);
-    mid = pack_bf16(r0, r1);
-    lo = pack_bf16(r0 - bf_lo(mid), r1 - bf_hi(mid));
+__device__ __forceinline__ void split3(float2 v, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
+    hi = pack_bf16(v);
+    const float2 r = sub2(v, bf2(hi));
+    mid = pack_bf16(r);
+    lo = pack_bf16(sub2(r, bf2(mid)));
 }
 
-__device__ __forceinline__ void su_cp16(uint32_t dst, const void* src, bool valid) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16u : 0u)
-                 : "memory");
+// A box of a tensor map (columns from x, token rows from y) into shared memory.
+__device__ __forceinline__ void su_tma(uint32_t dst, const CUtensorMap& map, int x, int y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+            dst),
+        "l"(&map), "r"(x), "r"(y), "r"(bar)
+        : "memory");
 }
 
 template <bool OUT>
-__global__ void __launch_bounds__(256, 2) k_scan_umma(const ScanArgs a, const int slices) {
+__global__ void __launch_bounds__(256, 2)
+    k_scan_umma(const ScanArgs a, const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mb,
+                const __grid_constant__ CUtensorMap mc, const int slices) {
     extern __shared__ __align__(1024) unsigned char smem[];
     const int H = a.s.H, P = a.s.P, N = a.s.N, G = a.s.G;
     const int hs = blockIdx.x % (H * slices), h = hs / slices, p0 = 64 * (hs - h * slices);
@@ -346,60 +376,48 @@ __global__ void __launch_bounds__(256, 2) k_scan_umma(const ScanArgs a, const in
         if (tid == 0) set_error(a.err, RSSM_DEVERR_TIMEOUT);
         return;
     }
-    const uint32_t bar_o = sb + kSuBar, bar_y = bar_o + 8, bar_u = bar_o + 16;
+    const uint32_t bar_in = sb + kSuBar, bar_s = bar_in + 8, bar_o = bar_in + 16, bar_y = bar_in + 24,
+                   bar_u = bar_in + 32;
+    volatile uint32_t* s_tmem = reinterpret_cast<volatile uint32_t*>(smem + kSuBar + 40);
     float* s_col = reinterpret_cast<float*>(smem + kSuCol);
     float* s_sum = reinterpret_cast<float*>(smem + kSuSum);
+    const bool wide = N > 64;  // B and C have a second block of 64 columns
+    const uint32_t in_bytes = kSuBlk * (1 + (wide ? 2u : 1u) * (OUT ? 2u : 1u));
+    const int xx = h * P + p0, bx = g * N;
+    auto load_c0 = [&](int t) { su_tma(sb + kSuC0, mc, bx, t, bar_in); };
+    auto load_x = [&](int t) { su_tma(sb + kSuX, mx, xx, t, bar_in); };
+    auto load_bc = [&](int t) {
+        su_tma(sb + kSuB, mb, bx, t, bar_in);
+        if (wide) su_tma(sb + kSuB + kSuBlk, mb, bx + 64, t, bar_in);
+        if (OUT && wide) su_tma(sb + kSuC1, mc, bx + 64, t, bar_in);
+    };
+    if (tid == 0) {
+        for (int i = 0; i < 5; ++i) mbar_init(bar_in + 8 * i, 1);
+        mbar_expect_tx(bar_in, in_bytes);
+        if (OUT) load_c0(it.t0);
+        load_x(it.t0);
+        load_bc(it.t0);
+    }
     if (warp == 0) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sb + kSuBar + 24),
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sb + kSuBar + 40),
                      "r"(kSuCols)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    if (tid == 0) {
-        mbar_init(bar_o, 1);
-        mbar_init(bar_y, 1);
-        mbar_init(bar_u, 1);
-    }
-
-    const __nv_bfloat16* xg = static_cast<const __nv_bfloat16*>(a.x) + static_cast<size_t>(h) * P + p0;
-    const __nv_bfloat16* Bg = static_cast<const __nv_bfloat16*>(a.B) + static_cast<size_t>(g) * N;
-    const __nv_bfloat16* Cg = static_cast<const __nv_bfloat16*>(a.C) + static_cast<size_t>(g) * N;
-    const size_t xstep = static_cast<size_t>(H) * P, bstep = static_cast<size_t>(G) * N;
-    // 64 columns from c0 of 128 token rows (tokens t0 ..) into the buffer at
-    // `buf`: row k's 16-byte chunk j at chunk j ^ (k & 7); zeros past the
-    // item's tokens and past column `cols`
-    auto fetch = [&](uint32_t buf, const __nv_bfloat16* src, size_t step, int t0, int c0, int cols) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int k = (tid >> 3) + 32 * i, j = tid & 7;
-            const bool ok = t0 + k < it.t1 && c0 + 8 * j < cols;
-            su_cp16(sb + buf + k * 128 + 16 * (j ^ (k & 7)), ok ? src + (t0 + k) * step + c0 + 8 * j : src, ok);
-        }
-    };
-    auto fetch_B = [&](int t0) {
-        fetch(kSuB, Bg, bstep, t0, 0, N);
-        if (N > 64) fetch(kSuB + kSuBlk, Bg, bstep, t0, 64, N);
-    };
     const float* dtg = a.dt + h;
     auto load_dt = [&](int t0) { return t0 + row < it.t1 ? dtg[static_cast<size_t>(t0 + row) * H] : 0.f; };
-
-    fetch_B(it.t0);
-    fetch(kSuX, xg, xstep, it.t0, 0, P - p0);
-    if (OUT) {
-        fetch(kSuC0, Cg, bstep, it.t0, 0, N);
-        if (N > 64) fetch(kSuC1, Cg, bstep, it.t0, 64, N);
-    }
     float dt = load_dt(it.t0);
-    const float A2 = a.A[h] * 1.4426950408889634f;  // decays as powers of two
+    // decays as powers of two; finite, so that a step of zero keeps all even then
+    const float A2 = a.A[h] * 1.4426950408889634f < -3e38f ? -3e38f : a.A[h] * 1.4426950408889634f;
     const float Dh = OUT ? a.D[h] : 0.f;
 
     // the state: row `row` (d_state), columns 32 half .. + 31 of the head_dim slice
-    float hst[32];
+    float2 hst[16];
     const float* init = it.slot < 0 ? head_state(a, it.b, h) : slot_state(a, it.slot, h);
     const int pb = p0 + 32 * half;  // this thread's first column
+    auto init_at = [&](int j) { return OUT && row < N && pb + j < P ? init[static_cast<size_t>(pb + j) * N + row] : 0.f; };
 #pragma unroll
-    for (int j = 0; j < 32; ++j)
-        hst[j] = OUT && row < N && pb + j < P ? init[static_cast<size_t>(pb + j) * N + row] : 0.f;
+    for (int j = 0; j < 16; ++j) hst[j] = make_float2(init_at(2 * j), init_at(2 * j + 1));
 
     // 16-byte chunk j of this thread's row in a buffer
     auto chunk = [&](uint32_t buf, int j) {
@@ -411,9 +429,8 @@ __global__ void __launch_bounds__(256, 2) k_scan_umma(const ScanArgs a, const in
             uint32_t hi[4], lo[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float v0 = hst[8 * j + 2 * i], v1 = hst[8 * j + 2 * i + 1];
-                hi[i] = pack_bf16(v0, v1);
-                lo[i] = pack_bf16(v0 - bf_lo(hi[i]), v1 - bf_hi(hi[i]));
+                hi[i] = pack_bf16(hst[4 * j + i]);
+                lo[i] = pack_bf16(sub2(hst[4 * j + i], bf2(hi[i])));
             }
             *chunk(kSuR, 4 * half + j) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
             *chunk(kSuR + kSuBlk, 4 * half + j) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
@@ -423,29 +440,43 @@ __global__ void __launch_bounds__(256, 2) k_scan_umma(const ScanArgs a, const in
     su_fence_before();
     __syncthreads();
     su_fence_after();
-    const uint32_t tm = *reinterpret_cast<volatile uint32_t*>(smem + kSuBar + 24);
+    const uint32_t tm = *s_tmem;
     const uint32_t tml = tm + (static_cast<uint32_t>(32 * q) << 16);  // this warp's lanes
+    const uint64_t dB = su_desc(sb + kSuB), dX = su_desc(sb + kSuX), dR = su_desc(sb + kSuR);
+    const uint64_t dC0 = su_desc(sb + kSuC0), dC1 = su_desc(sb + kSuC1);
     float dtsum = 0.f;
     bool timed_out = false;
 
     int par = 0;
     for (int t0 = it.t0; t0 < it.t1; t0 += kSuTok, par ^= 1) {
         const bool more = t0 + kSuTok < it.t1;
-        asm volatile("cp.async.wait_all;" ::: "memory");
+        if (!mbar_wait_bounded(bar_in, par, kWaitNs)) timed_out = true;
+        if (!more && t0 + row >= it.t1) {  // rows of the next request, or of none
+            const uint4 zero = make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) *chunk(kSuX, 4 * half + j) = zero;
+            if (wide || half == 0)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) *chunk(kSuB + half * kSuBlk, j) = zero;
+        }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         su_fence_before();
-        __syncthreads();  // the block and the state's parts are in place
+        if (__syncthreads_or(timed_out)) break;  // the block and the state's parts are in place
         su_fence_after();
         if (OUT && tid == 0) {
-            for (int ks = 0; ks < N / 16; ++ks) {
-                const uint32_t kc = (ks < 4 ? kSuC0 : kSuC1) + 32 * (ks & 3);
-                const uint32_t kb = kSuB + (ks < 4 ? 0u : kSuBlk) + 32 * (ks & 3);
-                su_mma<su_idesc(128, 0, 0)>(tm + kTmS, su_desc(sb + kc), su_desc(sb + kb), ks > 0);
-            }
-            for (int ks = 0; ks < N / 16; ++ks) {
-                const uint32_t kc = (ks < 4 ? kSuC0 : kSuC1) + 32 * (ks & 3);
-                su_mma<su_idesc(128, 0, 1)>(tm + kTmLo, su_desc(sb + kc), su_desc(sb + kSuR + 2048 * ks), ks > 0);
-            }
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks)
+                if (16 * ks < N)
+                    su_mma<su_idesc(128, 0, 0)>(tm + kTmS, (ks < 4 ? dC0 : dC1) + 2 * (ks & 3),
+                                                dB + (ks < 4 ? 0 : kSuBlk / 16) + 2 * (ks & 3), ks > 0);
+            su_commit(bar_s);
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks)
+                if (16 * ks < N) {
+                    const uint64_t c = (ks < 4 ? dC0 : dC1) + 2 * (ks & 3);
+                    su_mma<su_idesc(64, 0, 1)>(tm + kTmY, c, dR + 128 * ks, ks > 0);
+                    su_mma<su_idesc(64, 0, 1)>(tm + kTmY, c, dR + kSuBlk / 16 + 128 * ks, 1);
+                }
             su_commit(bar_o);
         }
         // decays of this thread's token within its 32-block
@@ -464,36 +495,7 @@ __global__ void __launch_bounds__(256, 2) k_scan_umma(const ScanArgs a, const in
             s_col[row] = col;
             if (lane == 0) s_sum[q] = suf;
         }
-        bool bad = false;
-        if (OUT) {
-            const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
-            __nv_bfloat162 z = zero;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const uint4 u = *chunk(kSuX, 4 * half + j);
-                z = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&u.x), zero, z);
-                z = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&u.y), zero, z);
-                z = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&u.z), zero, z);
-                z = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&u.w), zero, z);
-            }
-            bad = __hisnan(z.x) || __hisnan(z.y);
-        }
-        bad = __syncthreads_or(bad);  // and s_col, s_sum are written
-        if (bad) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                uint4* c = chunk(kSuX, 4 * half + j);
-                const uint4 u = *c;
-                *c = make_uint4(finite2(u.x), finite2(u.y), finite2(u.z), finite2(u.w));
-            }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        }
-        // chunk j of x of this block's token s, as given
-        auto x_given = [&](int s, int j) {
-            if (!bad) return *reinterpret_cast<const uint4*>(smem + kSuX + s * 128 + 16 * (j ^ (s & 7)));
-            if (t0 + s >= it.t1 || p0 + 8 * j >= P) return make_uint4(0, 0, 0, 0);
-            return *reinterpret_cast<const uint4*>(xg + (t0 + s) * xstep + 8 * j);
-        };
+        __syncthreads();  // s_col, s_sum
         float before = 0.f, after = 0.f;  // dt sums of the 32-blocks before and after this one
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -503,35 +505,31 @@ __global__ void __launch_bounds__(256, 2) k_scan_umma(const ScanArgs a, const in
         }
         const float total = s_sum[0] + s_sum[1] + s_sum[2] + s_sum[3];
 
-        float yo[32];
+        float2 yo[16];
+        bool bad = false;
+        // chunk j of x of this block's token s, as given
+        auto x_given = [&](int s, int j) {
+            if (!bad) return *reinterpret_cast<const uint4*>(smem + kSuX + s * 128 + 16 * (j ^ (s & 7)));
+            if (t0 + s >= it.t1 || p0 + 8 * j >= P) return make_uint4(0, 0, 0, 0);
+            return *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.x) +
+                                                   (static_cast<size_t>(t0 + s) * H + h) * P + p0 + 8 * j);
+        };
         if (OUT) {
             const float rowf = su_exp2(A2 * pre);
-            if (!mbar_wait_bounded(bar_o, par, kWaitNs)) timed_out = true;
+            if (!mbar_wait_bounded(bar_s, par, kWaitNs)) timed_out = true;
             su_fence_after();
-            // the state's share of the outputs, columns 32 half ..
-            const float fac = rowf * su_exp2(A2 * before);
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                uint32_t hi[16], lo[16];
-                su_ld16(tml + kTmLo + 32 * half + 16 * j, hi);
-                su_ld16(tml + kTmY + 32 * half + 16 * j, lo);
-                su_wait_ld();
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    yo[16 * j + i] = fac * (__uint_as_float(hi[i]) + __uint_as_float(lo[i]));
-            }
             // M over S, 32-blocks 2 half and 2 half + 1 of its columns, 16 at a
             // time: hi and mid parts in the columns read, lo in its own
-#pragma unroll
-            for (int jb = 1; jb >= 0; --jb) {
-                const int J = 2 * half + jb;
+#pragma unroll 1
+            for (int J = 2 * half + 1; J >= 2 * half; --J) {
+                const uint32_t tS = tml + kTmS + 32 * J, tL = tml + kTmLo + 16 * J;
                 if (J > q) {  // nothing but later tokens
                     const uint32_t zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        su_st8(tml + kTmS + 32 * J + 16 * k, zero);
-                        su_st8(tml + kTmS + 32 * J + 16 * k + 8, zero);
-                        su_st8(tml + kTmLo + 16 * J + 8 * k, zero);
+                        su_st8(tS + 16 * k, zero);
+                        su_st8(tS + 16 * k + 8, zero);
+                        su_st8(tL + 8 * k, zero);
                     }
                     continue;
                 }
@@ -539,68 +537,113 @@ __global__ void __launch_bounds__(256, 2) k_scan_umma(const ScanArgs a, const in
 #pragma unroll
                 for (int k = 1; k < 4; ++k) between += k > J && k < q ? s_sum[k] : 0.f;
                 const float rb = rowf * su_exp2(A2 * between);
-                float run = 0.f;  // dt sum from s + 1 to t
-#pragma unroll
+                const float2 rb2 = make_float2(rb, rb);
+                float run = 0.f;                                    // A2 times the dt sum from s + 1 to t
+                float dn = 0.f;                                     // dt of s + 1
+#pragma unroll 1
                 for (int k = 1; k >= 0; --k) {
                     uint32_t v[16];
-                    su_ld16(tml + kTmS + 32 * J + 16 * k, v);
-                    su_wait_ld();
-                    float m[16];
+                    su_ld16(tS + 16 * k, v);
+                    float2 m[8];
                     if (J == q) {
+                        float f[16];
 #pragma unroll
                         for (int i = 15; i >= 0; --i) {
                             const int s = 16 * k + i;
-                            if (s < 31) {
-                                const float dn = __shfl_sync(0xffffffffu, d, (s + 1) & 31);
-                                run += lane > s ? dn : 0.f;
-                            }
                             const float ds = __shfl_sync(0xffffffffu, d, s);
-                            const float f = lane == s ? ds : ds * su_exp2(A2 * run);
-                            m[i] = lane >= s ? __uint_as_float(v[i]) * f : 0.f;
+                            if (lane > s) run = fmaf(A2, dn, run);
+                            dn = ds;
+                            f[i] = ds * su_exp2(run);
+                        }
+                        su_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 16; i += 2) {
+                            const int s = 16 * k + i;
+                            m[i / 2] = make_float2(lane >= s ? __uint_as_float(v[i]) * f[i] : 0.f,
+                                                   lane > s ? __uint_as_float(v[i + 1]) * f[i + 1] : 0.f);
                         }
                     } else {
+                        const float4* c4 = reinterpret_cast<const float4*>(s_col + 32 * J + 16 * k);
+                        float2 f[8];
 #pragma unroll
-                        for (int i = 0; i < 16; i += 4) {
-                            const float4 c4 = *reinterpret_cast<const float4*>(s_col + 32 * J + 16 * k + i);
-                            m[i] = __uint_as_float(v[i]) * (rb * c4.x);
-                            m[i + 1] = __uint_as_float(v[i + 1]) * (rb * c4.y);
-                            m[i + 2] = __uint_as_float(v[i + 2]) * (rb * c4.z);
-                            m[i + 3] = __uint_as_float(v[i + 3]) * (rb * c4.w);
+                        for (int i = 0; i < 4; ++i) {
+                            const float4 c = c4[i];
+                            f[2 * i] = mul2(rb2, make_float2(c.x, c.y));
+                            f[2 * i + 1] = mul2(rb2, make_float2(c.z, c.w));
                         }
+                        su_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            m[i] = mul2(make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), f[i]);
                     }
                     uint32_t hi[8], mid[8], lo[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) split3(m[2 * i], m[2 * i + 1], hi[i], mid[i], lo[i]);
-                    su_st8(tml + kTmS + 32 * J + 16 * k, hi);
-                    su_st8(tml + kTmS + 32 * J + 16 * k + 8, mid);
-                    su_st8(tml + kTmLo + 16 * J + 8 * k, lo);
+                    for (int i = 0; i < 8; ++i) split3(m[i], hi[i], mid[i], lo[i]);
+                    su_st8(tS + 16 * k, hi);
+                    su_st8(tS + 16 * k + 8, mid);
+                    su_st8(tL + 8 * k, lo);
+                }
+            }
+            // the state's share of the outputs and D x, columns 32 half ..
+            const float fac = rowf * su_exp2(A2 * before);
+            const float2 fac2 = make_float2(fac, fac), Dh2 = make_float2(Dh, Dh);
+            const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
+            __nv_bfloat162 z = zero;  // NaN when x has a NaN or infinity
+            if (!mbar_wait_bounded(bar_o, par, kWaitNs)) timed_out = true;
+            su_fence_after();
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                uint32_t o[16];
+                su_ld16(tml + kTmY + 32 * half + 16 * j, o);
+                const uint4 u0 = *chunk(kSuX, 4 * half + 2 * j), u1 = *chunk(kSuX, 4 * half + 2 * j + 1);
+                const uint32_t xu[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
+                su_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    z = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&xu[i]), zero, z);
+                    yo[8 * j + i] = fma2(Dh2, bf2(xu[i]), mul2(fac2, make_float2(__uint_as_float(o[2 * i]),
+                                                                                 __uint_as_float(o[2 * i + 1]))));
                 }
             }
             su_wait_st();
             su_fence_before();
-            __syncthreads();  // M is complete; C and the state's parts have been read
+            bad = __syncthreads_or(__hisnan(z.x) || __hisnan(z.y));  // M is complete; C, O, the state's parts are read
+            if (bad) {
+#pragma unroll 1
+                for (int j = 0; j < 4; ++j) {
+                    uint4* c = chunk(kSuX, 4 * half + j);
+                    const uint4 u = *c;
+                    *c = make_uint4(finite2(u.x), finite2(u.y), finite2(u.z), finite2(u.w));
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncthreads();
+            }
             su_fence_after();
             if (tid == 0) {
+#pragma unroll
                 for (int ks = 0; ks < kSuTok / 16; ++ks) {
-                    const uint64_t xd = su_desc(sb + kSuX + 2048 * ks);
-                    su_mma_ts<su_idesc(64, 0, 1)>(tm + kTmY, tm + kTmS + 16 * ks, xd, ks > 0);
-                    su_mma_ts<su_idesc(64, 0, 1)>(tm + kTmY, tm + kTmS + 16 * ks + 8, xd, 1);
-                    su_mma_ts<su_idesc(64, 0, 1)>(tm + kTmY, tm + kTmLo + 8 * ks, xd, 1);
+                    su_mma_ts<su_idesc(64, 0, 1)>(tm + kTmY, tm + kTmS + 16 * ks, dX + 128 * ks, ks > 0);
+                    su_mma_ts<su_idesc(64, 0, 1)>(tm + kTmY, tm + kTmS + 16 * ks + 8, dX + 128 * ks, 1);
+                    su_mma_ts<su_idesc(64, 0, 1)>(tm + kTmY, tm + kTmLo + 8 * ks, dX + 128 * ks, 1);
                 }
                 su_commit(bar_y);
             }
-            if (more) fetch(kSuC0, Cg, bstep, t0 + kSuTok, 0, N);
+        }
+        if (tid == 0 && more) {
+            mbar_expect_tx(bar_in, in_bytes);
+            if (OUT) load_c0(t0 + kSuTok);
         }
         // w x in three parts
         {
             const float w = col * su_exp2(A2 * after);
-#pragma unroll
+            const float2 w2 = make_float2(w, w);
+#pragma unroll 1
             for (int j = 0; j < 4; ++j) {
                 const uint4 u = x_given(row, 4 * half + j);
                 const uint32_t xu[4] = {u.x, u.y, u.z, u.w};
                 uint32_t hi[4], mid[4], lo[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) split3(w * bf_lo(xu[i]), w * bf_hi(xu[i]), hi[i], mid[i], lo[i]);
+                for (int i = 0; i < 4; ++i) split3(mul2(w2, bf2(xu[i])), hi[i], mid[i], lo[i]);
                 *chunk(kSuR, 4 * half + j) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                 *chunk(kSuR + kSuBlk, 4 * half + j) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
                 *chunk(kSuC1, 4 * half + j) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
@@ -608,8 +651,7 @@ __global__ void __launch_bounds__(256, 2) k_scan_umma(const ScanArgs a, const in
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         su_fence_before();
-        __syncthreads();
-        su_fence_after();
+        __syncthreads();  // the parts of w x are in place, x has been read
         if (OUT && !mbar_wait_bounded(bar_y, par, kWaitNs)) timed_out = true;  // Y done, M read
         su_fence_after();
         if (OUT && bad) {  // what was left out of Y, 8 columns at a time, before U takes M's place
@@ -639,47 +681,47 @@ __global__ void __launch_bounds__(256, 2) k_scan_umma(const ScanArgs a, const in
                     }
                 }
 #pragma unroll
-                for (int i = 0; i < 8; ++i) yo[8 * j + i] += acc[i];
+                for (int i = 0; i < 4; ++i) yo[4 * j + i] = add2(yo[4 * j + i], make_float2(acc[2 * i], acc[2 * i + 1]));
             }
             su_fence_before();
             __syncthreads();
             su_fence_after();
         }
         if (tid == 0) {
+#pragma unroll
             for (int ks = 0; ks < kSuTok / 16; ++ks)
-                su_mma<su_idesc(192, 1, 1)>(tm + kTmS, su_desc(sb + kSuB + 2048 * ks), su_desc(sb + kSuR + 2048 * ks),
-                                            ks > 0);
+                su_mma<su_idesc(192, 1, 1)>(tm + kTmS, dB + 128 * ks, dR + 128 * ks, ks > 0);
             su_commit(bar_u);
+            if (more) load_x(t0 + kSuTok);
         }
         if (OUT) {
             const int t = t0 + row;
             float* yr = a.y + (static_cast<size_t>(t) * H + h) * P + pb;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                uint32_t v[8];
-                su_ld8(tml + kTmY + 32 * half + 8 * j, v);
+            for (int j = 0; j < 2; ++j) {
+                uint32_t v[16];
+                su_ld16(tml + kTmY + 32 * half + 16 * j, v);
                 su_wait_ld();
-                const uint4 u = x_given(row, 4 * half + j);
-                const float xv[8] = {bf_lo(u.x), bf_hi(u.x), bf_lo(u.y), bf_hi(u.y),
-                                     bf_lo(u.z), bf_hi(u.z), bf_lo(u.w), bf_hi(u.w)};
-                float o[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) o[i] = fmaf(Dh, xv[i], yo[8 * j + i]) + __uint_as_float(v[i]);
-                if (t < it.t1 && pb + 8 * j < P) {
-                    *reinterpret_cast<float4*>(yr + 8 * j) = make_float4(o[0], o[1], o[2], o[3]);
-                    *reinterpret_cast<float4*>(yr + 8 * j + 4) = make_float4(o[4], o[5], o[6], o[7]);
+                for (int i = 0; i < 2; ++i) {
+                    float2 o[4];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        o[c] = add2(yo[8 * j + 4 * i + c], make_float2(__uint_as_float(v[8 * i + 2 * c]),
+                                                                       __uint_as_float(v[8 * i + 2 * c + 1])));
+                    if (t < it.t1 && pb + 16 * j + 8 * i < P) {
+                        float4* to = reinterpret_cast<float4*>(yr + 16 * j + 8 * i);
+                        to[0] = make_float4(o[0].x, o[0].y, o[1].x, o[1].y);
+                        to[1] = make_float4(o[2].x, o[2].y, o[3].x, o[3].y);
+                    }
                 }
             }
         }
         if (!mbar_wait_bounded(bar_u, par, kWaitNs)) timed_out = true;
         su_fence_after();
-        __syncthreads();  // B, x and the parts of w x have been read
-        if (more) {
-            fetch_B(t0 + kSuTok);
-            fetch(kSuX, xg, xstep, t0 + kSuTok, 0, P - p0);
-            if (OUT && N > 64) fetch(kSuC1, Cg, bstep, t0 + kSuTok, 64, N);
-        }
+        if (tid == 0 && more) load_bc(t0 + kSuTok);  // U has read B and the parts of w x
         const float dec = su_exp2(A2 * total);
+        const float2 dec2 = make_float2(dec, dec);
         dtsum += total;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -689,9 +731,12 @@ __global__ void __launch_bounds__(256, 2) k_scan_umma(const ScanArgs a, const in
             su_ld8(tml + kTmS + 128 + 32 * half + 8 * j, u2);
             su_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                hst[8 * j + i] = fmaf(dec, hst[8 * j + i],
-                                      __uint_as_float(u0[i]) + (__uint_as_float(u1[i]) + __uint_as_float(u2[i])));
+            for (int i = 0; i < 4; ++i) {
+                auto two = [&](const uint32_t (&u)[8]) {
+                    return make_float2(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]));
+                };
+                hst[4 * j + i] = fma2(dec2, hst[4 * j + i], add2(two(u0), add2(two(u1), two(u2))));
+            }
         }
         if (OUT && more) put_state();
     }
@@ -699,8 +744,10 @@ __global__ void __launch_bounds__(256, 2) k_scan_umma(const ScanArgs a, const in
     if ((!OUT || it.last) && row < N) {
         float* out = OUT ? head_state(a, it.b, h) : slot_state(a, it.slot, h);
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-            if (pb + j < P) out[static_cast<size_t>(pb + j) * N + row] = hst[j];
+        for (int j = 0; j < 16; ++j) {
+            if (pb + 2 * j < P) out[static_cast<size_t>(pb + 2 * j) * N + row] = hst[j].x;
+            if (pb + 2 * j + 1 < P) out[static_cast<size_t>(pb + 2 * j + 1) * N + row] = hst[j].y;
+        }
     }
     if (!OUT && tid == 0 && p0 == 0) *slot_dtsum(a, it.slot, h) = dtsum;
     su_fence_before();
@@ -743,14 +790,49 @@ bool scan_umma_shape(const Shape& s, int in_bf16) {
     return in_bf16 && s.P % 8 == 0 && static_cast<long long>(s.batch) * s.H * ((s.P + 63) / 64) <= 0x7fffffffLL;
 }
 
+// The driver's tensor-map encoder (the library links the runtime only).
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiled encode_tiled() {
+    static std::atomic<void*> fn{nullptr};
+    void* p = fn.load(std::memory_order_acquire);
+    if (!p) {
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            return nullptr;
+        fn.store(p, std::memory_order_release);
+    }
+    return reinterpret_cast<EncodeTiled>(p);
+}
+
+// Per-token rows [total][width] bf16, read in boxes of 128 tokens x 64
+// columns (128-byte rows, swizzled); zeros outside.
+bool encode_rows(CUtensorMap* m, const void* base, int total, long long width) {
+    EncodeTiled fn = encode_tiled();
+    if (!fn) return false;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(total)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(2 * width)};
+    const cuuint32_t box[2] = {64, kSuTok}, es[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <bool OUT>
 cudaError_t launch_umma(const ScanArgs& a, int items, cudaStream_t st) {
     const int slices = (a.s.P + 63) / 64;
+    CUtensorMap mx, mb, mc;
+    const long long xw = static_cast<long long>(a.s.H) * a.s.P, bw = static_cast<long long>(a.s.G) * a.s.N;
+    if (!encode_rows(&mx, a.x, a.total, xw) || !encode_rows(&mb, a.B, a.total, bw) ||
+        !encode_rows(&mc, a.C, a.total, bw))
+        return cudaErrorInvalidValue;
     cudaError_t e = cudaFuncSetAttribute(k_scan_umma<OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(kSuSmem));
     if (e != cudaSuccess) return e;
     const dim3 grid(static_cast<unsigned>(items) * static_cast<unsigned>(a.s.H) * static_cast<unsigned>(slices));
-    k_scan_umma<OUT><<<grid, 256, kSuSmem, st>>>(a, slices);
+    k_scan_umma<OUT><<<grid, 256, kSuSmem, st>>>(a, mx, mb, mc, slices);
     return cudaGetLastError();
 }
 
