@@ -227,6 +227,8 @@ __global__ void __launch_bounds__(kThreads) k_scan(const ScanArgs a) {
 // output before them changes.
 // ---------------------------------------------------------------------------
 constexpr int kSuTok = 128;                    // tokens per block
+constexpr int kSuThreads = 512;
+constexpr int kSuIssuer = 12;                  // a warp with none of M's lower triangle
 constexpr uint32_t kSuBlk = kSuTok * 128u;     // 128 rows of 128 bytes, swizzled: 16 KB
 constexpr uint32_t kSuB = 0;                   // B rows, two 64-column blocks
 constexpr uint32_t kSuX = 2 * kSuBlk;          // x rows
@@ -302,6 +304,18 @@ __device__ __forceinline__ void su_st8(uint32_t taddr, const uint32_t (&r)[8]) {
                  : "memory");
 }
 
+__device__ __forceinline__ void su_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+        "%14, %15};" ::"r"(r[0]),
+        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+        "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void su_ld1(uint32_t taddr, uint32_t& r) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr));
+}
+
 __device__ __forceinline__ float su_exp2(float v) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
@@ -359,18 +373,38 @@ __device__ __forceinline__ void su_tma(uint32_t dst, const CUtensorMap& map, int
         : "memory");
 }
 
+// One lane of a warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
+
+// 32 fp32 columns from x of head h, 128 tokens from t, out of shared memory;
+// what lies past the tensor is not written.
+__device__ __forceinline__ void su_tma_store(const CUtensorMap& map, uint32_t src, int x, int h, int t) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(&map), "r"(src),
+                 "r"(x), "r"(h), "r"(t)
+                 : "memory");
+}
+
 template <bool OUT>
-__global__ void __launch_bounds__(256, 2)
+__global__ void __launch_bounds__(kSuThreads, 2)
     k_scan_umma(const ScanArgs a, const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mb,
-                const __grid_constant__ CUtensorMap mc, const int slices) {
+                const __grid_constant__ CUtensorMap mc, const __grid_constant__ CUtensorMap my, const int slices) {
     extern __shared__ __align__(1024) unsigned char smem[];
     const int H = a.s.H, P = a.s.P, N = a.s.N, G = a.s.G;
     const int hs = blockIdx.x % (H * slices), h = hs / slices, p0 = 64 * (hs - h * slices);
     Item it;
     if (!find_item<OUT>(a, blockIdx.x / (H * slices), it)) return;
-    const int g = h / (H / G), tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int q = warp & 3, half = warp >> 2;  // rows 32 q .., columns of half `half`
-    const int row = 32 * q + lane;             // this thread's token and state row
+    const int g = h / (H / G), tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+    const int q = warp & 3, J = warp >> 2;  // rows 32 q .., 32-block J of M's columns, columns 16 J .. elsewhere
+    const int row = 32 * q + lane;          // this thread's token and state row
     const uint32_t sb = smem_u32(smem);
     if (sb & 1023u) {  // the swizzled operands lie on 1024-byte boundaries
         if (tid == 0) set_error(a.err, RSSM_DEVERR_TIMEOUT);
@@ -379,11 +413,10 @@ __global__ void __launch_bounds__(256, 2)
     const uint32_t bar_in = sb + kSuBar, bar_s = bar_in + 8, bar_o = bar_in + 16, bar_y = bar_in + 24,
                    bar_u = bar_in + 32;
     volatile uint32_t* s_tmem = reinterpret_cast<volatile uint32_t*>(smem + kSuBar + 40);
-    float* s_col = reinterpret_cast<float*>(smem + kSuCol);
-    float* s_sum = reinterpret_cast<float*>(smem + kSuSum);
     const bool wide = N > 64;  // B and C have a second block of 64 columns
     const uint32_t in_bytes = kSuBlk * (1 + (wide ? 2u : 1u) * (OUT ? 2u : 1u));
     const int xx = h * P + p0, bx = g * N;
+    const bool issuer = warp == kSuIssuer;  // its elected lane issues every copy and product
     auto load_c0 = [&](int t) { su_tma(sb + kSuC0, mc, bx, t, bar_in); };
     auto load_x = [&](int t) { su_tma(sb + kSuX, mx, xx, t, bar_in); };
     auto load_bc = [&](int t) {
@@ -391,7 +424,7 @@ __global__ void __launch_bounds__(256, 2)
         if (wide) su_tma(sb + kSuB + kSuBlk, mb, bx + 64, t, bar_in);
         if (OUT && wide) su_tma(sb + kSuC1, mc, bx + 64, t, bar_in);
     };
-    if (tid == 0) {
+    if (issuer && elect_one()) {
         for (int i = 0; i < 5; ++i) mbar_init(bar_in + 8 * i, 1);
         mbar_expect_tx(bar_in, in_bytes);
         if (OUT) load_c0(it.t0);
@@ -406,18 +439,18 @@ __global__ void __launch_bounds__(256, 2)
     }
     const float* dtg = a.dt + h;
     auto load_dt = [&](int t0) { return t0 + row < it.t1 ? dtg[static_cast<size_t>(t0 + row) * H] : 0.f; };
-    float dt = load_dt(it.t0);
+    float d = load_dt(it.t0);
     // decays as powers of two; finite, so that a step of zero keeps all even then
     const float A2 = a.A[h] * 1.4426950408889634f < -3e38f ? -3e38f : a.A[h] * 1.4426950408889634f;
     const float Dh = OUT ? a.D[h] : 0.f;
 
-    // the state: row `row` (d_state), columns 32 half .. + 31 of the head_dim slice
-    float2 hst[16];
+    // the state: row `row` (d_state), columns 16 J .. + 15 of the head_dim slice
+    float2 hst[8];
     const float* init = it.slot < 0 ? head_state(a, it.b, h) : slot_state(a, it.slot, h);
-    const int pb = p0 + 32 * half;  // this thread's first column
+    const int pb = p0 + 16 * J;  // this thread's first column
     auto init_at = [&](int j) { return OUT && row < N && pb + j < P ? init[static_cast<size_t>(pb + j) * N + row] : 0.f; };
 #pragma unroll
-    for (int j = 0; j < 16; ++j) hst[j] = make_float2(init_at(2 * j), init_at(2 * j + 1));
+    for (int j = 0; j < 8; ++j) hst[j] = make_float2(init_at(2 * j), init_at(2 * j + 1));
 
     // 16-byte chunk j of this thread's row in a buffer
     auto chunk = [&](uint32_t buf, int j) {
@@ -425,64 +458,22 @@ __global__ void __launch_bounds__(256, 2)
     };
     auto put_state = [&]() {  // hi and lo parts of the state, d_state row by row
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < 2; ++j) {
             uint32_t hi[4], lo[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 hi[i] = pack_bf16(hst[4 * j + i]);
                 lo[i] = pack_bf16(sub2(hst[4 * j + i], bf2(hi[i])));
             }
-            *chunk(kSuR, 4 * half + j) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *chunk(kSuR + kSuBlk, 4 * half + j) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            *chunk(kSuR, 2 * J + j) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *chunk(kSuR + kSuBlk, 2 * J + j) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
     };
-    if (OUT) put_state();
-    su_fence_before();
-    __syncthreads();
-    su_fence_after();
-    const uint32_t tm = *s_tmem;
-    const uint32_t tml = tm + (static_cast<uint32_t>(32 * q) << 16);  // this warp's lanes
-    const uint64_t dB = su_desc(sb + kSuB), dX = su_desc(sb + kSuX), dR = su_desc(sb + kSuR);
-    const uint64_t dC0 = su_desc(sb + kSuC0), dC1 = su_desc(sb + kSuC1);
-    float dtsum = 0.f;
-    bool timed_out = false;
-
-    int par = 0;
-    for (int t0 = it.t0; t0 < it.t1; t0 += kSuTok, par ^= 1) {
-        const bool more = t0 + kSuTok < it.t1;
-        if (!mbar_wait_bounded(bar_in, par, kWaitNs)) timed_out = true;
-        if (!more && t0 + row >= it.t1) {  // rows of the next request, or of none
-            const uint4 zero = make_uint4(0, 0, 0, 0);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) *chunk(kSuX, 4 * half + j) = zero;
-            if (wide || half == 0)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) *chunk(kSuB + half * kSuBlk, j) = zero;
-        }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        su_fence_before();
-        if (__syncthreads_or(timed_out)) break;  // the block and the state's parts are in place
-        su_fence_after();
-        if (OUT && tid == 0) {
-#pragma unroll
-            for (int ks = 0; ks < 8; ++ks)
-                if (16 * ks < N)
-                    su_mma<su_idesc(128, 0, 0)>(tm + kTmS, (ks < 4 ? dC0 : dC1) + 2 * (ks & 3),
-                                                dB + (ks < 4 ? 0 : kSuBlk / 16) + 2 * (ks & 3), ks > 0);
-            su_commit(bar_s);
-#pragma unroll
-            for (int ks = 0; ks < 8; ++ks)
-                if (16 * ks < N) {
-                    const uint64_t c = (ks < 4 ? dC0 : dC1) + 2 * (ks & 3);
-                    su_mma<su_idesc(64, 0, 1)>(tm + kTmY, c, dR + 128 * ks, ks > 0);
-                    su_mma<su_idesc(64, 0, 1)>(tm + kTmY, c, dR + kSuBlk / 16 + 128 * ks, 1);
-                }
-            su_commit(bar_o);
-        }
-        // decays of this thread's token within its 32-block
-        const float d = dt;
-        if (more) dt = load_dt(t0 + kSuTok);
-        float pre = d, suf = d;  // inclusive sums from the block's start, to its end
+    // decays of this thread's token within its 32-block, from d
+    float* s_col = reinterpret_cast<float*>(smem + kSuCol);
+    float rowf;
+    auto scan_dt = [&]() {
+        float pre = d, suf = d;  // inclusive sums from the 32-block's start, to its end
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
             const float u = __shfl_up_sync(0xffffffffu, pre, off), v = __shfl_down_sync(0xffffffffu, suf, off);
@@ -490,91 +481,123 @@ __global__ void __launch_bounds__(256, 2)
             if (lane + off < 32) suf += v;
         }
         const float next = __shfl_down_sync(0xffffffffu, suf, 1);
-        const float col = d * su_exp2(A2 * (lane == 31 ? 0.f : next));
-        if (half == 0) {
-            s_col[row] = col;
-            if (lane == 0) s_sum[q] = suf;
+        rowf = su_exp2(A2 * pre);
+        if (J == 0) {
+            s_col[row] = d * su_exp2(A2 * (lane == 31 ? 0.f : next));
+            if (lane == 0) reinterpret_cast<float*>(smem + kSuSum)[q] = suf;
         }
-        __syncthreads();  // s_col, s_sum
-        float before = 0.f, after = 0.f;  // dt sums of the 32-blocks before and after this one
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float s = s_sum[k];
-            before += k < q ? s : 0.f;
-            after += k > q ? s : 0.f;
-        }
-        const float total = s_sum[0] + s_sum[1] + s_sum[2] + s_sum[3];
+    };
+    if (OUT) put_state();
+    scan_dt();
+    su_fence_before();
+    __syncthreads();
+    su_fence_after();
+    const uint32_t tm = __shfl_sync(0xffffffffu, *s_tmem, 0);
+    const uint32_t tml = tm + (static_cast<uint32_t>(32 * q) << 16);  // this warp's lanes
+    float dtsum = 0.f;
+    bool timed_out = false;
 
-        float2 yo[16];
-        bool bad = false;
+    int par = 0;
+    for (int t0 = it.t0; t0 < it.t1; t0 += kSuTok, par ^= 1) {
+        const bool more = t0 + kSuTok < it.t1;
+        const float dn = more ? load_dt(t0 + kSuTok) : 0.f;
+        if (!mbar_wait_bounded(bar_in, par, kWaitNs)) timed_out = true;
+        if (!more && t0 + row >= it.t1) {  // rows of the next request, or of none
+            const uint4 zero = make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) *chunk(kSuX, 2 * J + j) = zero;
+            if (wide || J < 2)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) *chunk(kSuB + (J >> 1) * kSuBlk, 4 * (J & 1) + j) = zero;
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        su_fence_before();
+        if (__syncthreads_or(timed_out)) break;  // the block, its decays and the state's parts are in place
+        su_fence_after();
+        if (OUT && issuer) {
+            const uint64_t dB = su_desc(sb + kSuB), dR = su_desc(sb + kSuR);
+            const uint64_t dC0 = su_desc(sb + kSuC0), dC1 = su_desc(sb + kSuC1);
+            if (elect_one()) {
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks)
+                    if (16 * ks < N)
+                        su_mma<su_idesc(128, 0, 0)>(tm + kTmS, (ks < 4 ? dC0 : dC1) + 2 * (ks & 3),
+                                                    dB + (ks < 4 ? 0 : kSuBlk / 16) + 2 * (ks & 3), ks > 0);
+                su_commit(bar_s);
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks)
+                    if (16 * ks < N) {
+                        const uint64_t c = (ks < 4 ? dC0 : dC1) + 2 * (ks & 3);
+                        su_mma<su_idesc(64, 0, 1)>(tm + kTmY, c, dR + 128 * ks, ks > 0);
+                        su_mma<su_idesc(64, 0, 1)>(tm + kTmY, c, dR + kSuBlk / 16 + 128 * ks, 1);
+                    }
+                su_commit(bar_o);
+            }
+            __syncwarp();
+        }
+        const float4 sums = *reinterpret_cast<const float4*>(smem + kSuSum);  // of the 32-blocks' dt
+        const float total = sums.x + sums.y + sums.z + sums.w;
+
         // chunk j of x of this block's token s, as given
         auto x_given = [&](int s, int j) {
-            if (!bad) return *reinterpret_cast<const uint4*>(smem + kSuX + s * 128 + 16 * (j ^ (s & 7)));
             if (t0 + s >= it.t1 || p0 + 8 * j >= P) return make_uint4(0, 0, 0, 0);
             return *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.x) +
                                                    (static_cast<size_t>(t0 + s) * H + h) * P + p0 + 8 * j);
         };
         if (OUT) {
-            const float rowf = su_exp2(A2 * pre);
+            // dt sums of the 32-blocks before this thread's token's, and between J and it
+            const float before = (q > 0 ? sums.x : 0.f) + (q > 1 ? sums.y : 0.f) + (q > 2 ? sums.z : 0.f);
+            const float between = (J < 1 && q > 1 ? sums.y : 0.f) + (J < 2 && q > 2 ? sums.z : 0.f);
+            const float rb = rowf * su_exp2(A2 * between);
             if (!mbar_wait_bounded(bar_s, par, kWaitNs)) timed_out = true;
             su_fence_after();
-            // M over S, 32-blocks 2 half and 2 half + 1 of its columns, 16 at a
-            // time: hi and mid parts in the columns read, lo in its own
-#pragma unroll 1
-            for (int J = 2 * half + 1; J >= 2 * half; --J) {
-                const uint32_t tS = tml + kTmS + 32 * J, tL = tml + kTmLo + 16 * J;
-                if (J > q) {  // nothing but later tokens
-                    const uint32_t zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+            // M over S, 32-block J of its columns, 16 at a time: hi and mid parts
+            // in the columns read, lo in its own
+            const uint32_t tS = tml + kTmS + 32 * J, tL = tml + kTmLo + 16 * J;
+            if (J > q) {  // nothing but later tokens
+                const uint32_t zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        su_st8(tS + 16 * k, zero);
-                        su_st8(tS + 16 * k + 8, zero);
-                        su_st8(tL + 8 * k, zero);
-                    }
-                    continue;
+                for (int k = 0; k < 2; ++k) {
+                    su_st8(tS + 16 * k, zero);
+                    su_st8(tS + 16 * k + 8, zero);
+                    su_st8(tL + 8 * k, zero);
                 }
-                float between = 0.f;
-#pragma unroll
-                for (int k = 1; k < 4; ++k) between += k > J && k < q ? s_sum[k] : 0.f;
-                const float rb = rowf * su_exp2(A2 * between);
+            } else {
                 const float2 rb2 = make_float2(rb, rb);
-                float run = 0.f;                                    // A2 times the dt sum from s + 1 to t
-                float dn = 0.f;                                     // dt of s + 1
+                float run = 0.f;   // A2 times the dt sum from s + 1 to t
+                float dnx = 0.f;   // dt of s + 1
 #pragma unroll 1
                 for (int k = 1; k >= 0; --k) {
                     uint32_t v[16];
                     su_ld16(tS + 16 * k, v);
                     float2 m[8];
                     if (J == q) {
-                        float f[16];
+                        su_wait_ld();
 #pragma unroll
                         for (int i = 15; i >= 0; --i) {
                             const int s = 16 * k + i;
                             const float ds = __shfl_sync(0xffffffffu, d, s);
-                            if (lane > s) run = fmaf(A2, dn, run);
-                            dn = ds;
-                            f[i] = ds * su_exp2(run);
-                        }
-                        su_wait_ld();
-#pragma unroll
-                        for (int i = 0; i < 16; i += 2) {
-                            const int s = 16 * k + i;
-                            m[i / 2] = make_float2(lane >= s ? __uint_as_float(v[i]) * f[i] : 0.f,
-                                                   lane > s ? __uint_as_float(v[i + 1]) * f[i + 1] : 0.f);
+                            if (lane > s) run = fmaf(A2, dnx, run);
+                            dnx = ds;
+                            const float f = ds * su_exp2(run);
+                            float e = lane >= s ? __uint_as_float(v[i]) * f : 0.f;
+                            if (lane == s) e += Dh;  // D x_t
+                            if (i & 1)
+                                m[i / 2].y = e;
+                            else
+                                m[i / 2].x = e;
                         }
                     } else {
                         const float4* c4 = reinterpret_cast<const float4*>(s_col + 32 * J + 16 * k);
-                        float2 f[8];
+                        su_wait_ld();
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const float4 c = c4[i];
-                            f[2 * i] = mul2(rb2, make_float2(c.x, c.y));
-                            f[2 * i + 1] = mul2(rb2, make_float2(c.z, c.w));
+                            m[2 * i] = mul2(make_float2(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1])),
+                                            mul2(rb2, make_float2(c.x, c.y)));
+                            m[2 * i + 1] = mul2(make_float2(__uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3])),
+                                                mul2(rb2, make_float2(c.z, c.w)));
                         }
-                        su_wait_ld();
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            m[i] = mul2(make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), f[i]);
                     }
                     uint32_t hi[8], mid[8], lo[8];
 #pragma unroll
@@ -584,151 +607,180 @@ __global__ void __launch_bounds__(256, 2)
                     su_st8(tL + 8 * k, lo);
                 }
             }
-            // the state's share of the outputs and D x, columns 32 half ..
+            // the state's share of the outputs, scaled in place; Y is added to it
             const float fac = rowf * su_exp2(A2 * before);
-            const float2 fac2 = make_float2(fac, fac), Dh2 = make_float2(Dh, Dh);
-            const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
-            __nv_bfloat162 z = zero;  // NaN when x has a NaN or infinity
+            const float2 fac2 = make_float2(fac, fac);
             if (!mbar_wait_bounded(bar_o, par, kWaitNs)) timed_out = true;
             su_fence_after();
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
+            {
                 uint32_t o[16];
-                su_ld16(tml + kTmY + 32 * half + 16 * j, o);
-                const uint4 u0 = *chunk(kSuX, 4 * half + 2 * j), u1 = *chunk(kSuX, 4 * half + 2 * j + 1);
-                const uint32_t xu[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
+                su_ld16(tml + kTmY + 16 * J, o);
                 su_wait_ld();
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    z = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&xu[i]), zero, z);
-                    yo[8 * j + i] = fma2(Dh2, bf2(xu[i]), mul2(fac2, make_float2(__uint_as_float(o[2 * i]),
-                                                                                 __uint_as_float(o[2 * i + 1]))));
+                    const float2 v = mul2(fac2, make_float2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1])));
+                    o[2 * i] = __float_as_uint(v.x);
+                    o[2 * i + 1] = __float_as_uint(v.y);
                 }
+                su_st16(tml + kTmY + 16 * J, o);
             }
             su_wait_st();
-            su_fence_before();
-            bad = __syncthreads_or(__hisnan(z.x) || __hisnan(z.y));  // M is complete; C, O, the state's parts are read
-            if (bad) {
+        }
+        // w x in three parts. The warps of rows 32 q .. have the more of M the
+        // larger q: those of q = 0 take 3 of the 8 passes over 16 token rows,
+        // the others 2, 2 and 1, a 16-byte chunk per thread and pass.
+        const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
+        __nv_bfloat162 z = zero;  // NaN when x has a NaN or infinity
 #pragma unroll 1
-                for (int j = 0; j < 4; ++j) {
-                    uint4* c = chunk(kSuX, 4 * half + j);
-                    const uint4 u = *c;
-                    *c = make_uint4(finite2(u.x), finite2(u.y), finite2(u.z), finite2(u.w));
-                }
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                __syncthreads();
-            }
-            su_fence_after();
-            if (tid == 0) {
-#pragma unroll
-                for (int ks = 0; ks < kSuTok / 16; ++ks) {
-                    su_mma_ts<su_idesc(64, 0, 1)>(tm + kTmY, tm + kTmS + 16 * ks, dX + 128 * ks, ks > 0);
-                    su_mma_ts<su_idesc(64, 0, 1)>(tm + kTmY, tm + kTmS + 16 * ks + 8, dX + 128 * ks, 1);
-                    su_mma_ts<su_idesc(64, 0, 1)>(tm + kTmY, tm + kTmLo + 8 * ks, dX + 128 * ks, 1);
-                }
-                su_commit(bar_y);
-            }
-        }
-        if (tid == 0 && more) {
-            mbar_expect_tx(bar_in, in_bytes);
-            if (OUT) load_c0(t0 + kSuTok);
-        }
-        // w x in three parts
-        {
-            const float w = col * su_exp2(A2 * after);
+        for (int pass = q == 0 ? 0 : 2 * q + 1, end = q == 3 ? 8 : 2 * q + 3; pass < end; ++pass) {
+            const int s = 16 * pass + 4 * J + (lane >> 3);
+            const uint32_t at = static_cast<uint32_t>(128 * s + 16 * ((lane & 7) ^ (s & 7)));
+            const uint4 u = *reinterpret_cast<const uint4*>(smem + kSuX + at);
+            // dt sum of the 32-blocks after the token's
+            const float after = (pass < 2 ? sums.y : 0.f) + (pass < 4 ? sums.z : 0.f) + (pass < 6 ? sums.w : 0.f);
+            const float w = s_col[s] * su_exp2(A2 * after);
             const float2 w2 = make_float2(w, w);
-#pragma unroll 1
-            for (int j = 0; j < 4; ++j) {
-                const uint4 u = x_given(row, 4 * half + j);
-                const uint32_t xu[4] = {u.x, u.y, u.z, u.w};
-                uint32_t hi[4], mid[4], lo[4];
+            const uint32_t xu[4] = {u.x, u.y, u.z, u.w};
+            uint32_t hi[4], mid[4], lo[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) split3(mul2(w2, bf2(xu[i])), hi[i], mid[i], lo[i]);
-                *chunk(kSuR, 4 * half + j) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                *chunk(kSuR + kSuBlk, 4 * half + j) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
-                *chunk(kSuC1, 4 * half + j) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            for (int i = 0; i < 4; ++i) {
+                if (OUT) z = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&xu[i]), zero, z);
+                split3(mul2(w2, bf2(xu[i])), hi[i], mid[i], lo[i]);
             }
+            *reinterpret_cast<uint4*>(smem + kSuR + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(smem + kSuR + kSuBlk + at) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
+            *reinterpret_cast<uint4*>(smem + kSuC1 + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         su_fence_before();
-        __syncthreads();  // the parts of w x are in place, x has been read
-        if (OUT && !mbar_wait_bounded(bar_y, par, kWaitNs)) timed_out = true;  // Y done, M read
+        // M and the parts of w x are in place, x, C and the state's parts have been read
+        const bool bad = __syncthreads_or(OUT && (__hisnan(z.x) || __hisnan(z.y)));
+        if (OUT && bad) {
+#pragma unroll 1
+            for (int j = 0; j < 2; ++j) {
+                uint4* c = chunk(kSuX, 2 * J + j);
+                const uint4 u = *c;
+                *c = make_uint4(finite2(u.x), finite2(u.y), finite2(u.z), finite2(u.w));
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncthreads();
+        }
         su_fence_after();
-        if (OUT && bad) {  // what was left out of Y, 8 columns at a time, before U takes M's place
+        if (OUT) {
+            if (issuer) {
+                const uint64_t dX = su_desc(sb + kSuX);
+                if (elect_one()) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+                    for (int ks = 0; ks < kSuTok / 16; ++ks) {
+                        su_mma_ts<su_idesc(64, 0, 1)>(tm + kTmY, tm + kTmS + 16 * ks, dX + 128 * ks, 1);
+                        su_mma_ts<su_idesc(64, 0, 1)>(tm + kTmY, tm + kTmS + 16 * ks + 8, dX + 128 * ks, 1);
+                        su_mma_ts<su_idesc(64, 0, 1)>(tm + kTmY, tm + kTmLo + 8 * ks, dX + 128 * ks, 1);
+                    }
+                    su_commit(bar_y);
+                }
+                __syncwarp();
+            }
+        }
+        d = dn;
+        if (more) scan_dt();
+        if (OUT) {
+            if (!mbar_wait_bounded(bar_y, par, kWaitNs)) timed_out = true;  // Y done, M and x read
+            su_fence_after();
+        }
+        if (OUT && bad) {  // what was left out of Y, 8 columns at a time, before U takes M's place
+#pragma unroll 1
+            for (int j = 0; j < 2; ++j) {
                 float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll 1
-                for (int ks = 0; ks < kSuTok / 16; ++ks) {
-                    uint32_t hi[8], mid[8], lo[8];
-                    su_ld8(tml + kTmS + 16 * ks, hi);
-                    su_ld8(tml + kTmS + 16 * ks + 8, mid);
-                    su_ld8(tml + kTmLo + 8 * ks, lo);
+                for (int s = 0; s < kSuTok; ++s) {
+                    uint32_t hi, mid, lo;
+                    su_ld1(tml + kTmS + 16 * (s >> 4) + ((s & 15) >> 1), hi);
+                    su_ld1(tml + kTmS + 16 * (s >> 4) + 8 + ((s & 15) >> 1), mid);
+                    su_ld1(tml + kTmLo + (s >> 1), lo);
                     su_wait_ld();
+                    const float m = s & 1 ? bf_hi(hi) + (bf_hi(mid) + bf_hi(lo)) : bf_lo(hi) + (bf_lo(mid) + bf_lo(lo));
+                    const uint4 u = x_given(s, 2 * J + j);
+                    const uint32_t xu[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const int s = 16 * ks + i;
-                        const float m = i & 1 ? bf_hi(hi[i / 2]) + (bf_hi(mid[i / 2]) + bf_hi(lo[i / 2]))
-                                              : bf_lo(hi[i / 2]) + (bf_lo(mid[i / 2]) + bf_lo(lo[i / 2]));
-                        const uint4 u = x_given(s, 4 * half + j);
-                        const uint32_t xu[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            const uint32_t out = finite2(xu[c]) ^ xu[c];
-                            if (s <= row && (out & 0xFFFFu)) acc[2 * c] = fmaf(m, bf_lo(xu[c]), acc[2 * c]);
-                            if (s <= row && (out >> 16)) acc[2 * c + 1] = fmaf(m, bf_hi(xu[c]), acc[2 * c + 1]);
-                        }
+                    for (int c = 0; c < 4; ++c) {
+                        const uint32_t out = finite2(xu[c]) ^ xu[c];
+                        if (s <= row && (out & 0xFFFFu)) acc[2 * c] = fmaf(m, bf_lo(xu[c]), acc[2 * c]);
+                        if (s <= row && (out >> 16)) acc[2 * c + 1] = fmaf(m, bf_hi(xu[c]), acc[2 * c + 1]);
                     }
                 }
+                uint32_t y[8];
+                su_ld8(tml + kTmY + 16 * J + 8 * j, y);
+                su_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 4; ++i) yo[4 * j + i] = add2(yo[4 * j + i], make_float2(acc[2 * i], acc[2 * i + 1]));
+                for (int i = 0; i < 8; ++i) y[i] = __float_as_uint(__uint_as_float(y[i]) + acc[i]);
+                su_st8(tml + kTmY + 16 * J + 8 * j, y);
             }
+            su_wait_st();
             su_fence_before();
             __syncthreads();
             su_fence_after();
         }
-        if (tid == 0) {
+        if (issuer) {
+            const uint64_t dB = su_desc(sb + kSuB), dR = su_desc(sb + kSuR);
+            if (elect_one()) {
 #pragma unroll
-            for (int ks = 0; ks < kSuTok / 16; ++ks)
-                su_mma<su_idesc(192, 1, 1)>(tm + kTmS, dB + 128 * ks, dR + 128 * ks, ks > 0);
-            su_commit(bar_u);
-            if (more) load_x(t0 + kSuTok);
+                for (int ks = 0; ks < kSuTok / 16; ++ks)
+                    su_mma<su_idesc(192, 1, 1)>(tm + kTmS, dB + 128 * ks, dR + 128 * ks, ks > 0);
+                su_commit(bar_u);
+            }
+            __syncwarp();
         }
         if (OUT) {
-            const int t = t0 + row;
-            float* yr = a.y + (static_cast<size_t>(t) * H + h) * P + pb;
+            // Y by way of the buffers of x and C's first half, 32 columns each
+            uint32_t y[16];
+            su_ld16(tml + kTmY + 16 * J, y);
+            su_wait_ld();
+            const uint32_t buf = J < 2 ? kSuX : kSuC0;
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                uint32_t v[16];
-                su_ld16(tml + kTmY + 32 * half + 16 * j, v);
-                su_wait_ld();
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    float2 o[4];
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        o[c] = add2(yo[8 * j + 4 * i + c], make_float2(__uint_as_float(v[8 * i + 2 * c]),
-                                                                       __uint_as_float(v[8 * i + 2 * c + 1])));
-                    if (t < it.t1 && pb + 16 * j + 8 * i < P) {
-                        float4* to = reinterpret_cast<float4*>(yr + 16 * j + 8 * i);
-                        to[0] = make_float4(o[0].x, o[0].y, o[1].x, o[1].y);
-                        to[1] = make_float4(o[2].x, o[2].y, o[3].x, o[3].y);
-                    }
+            for (int i = 0; i < 4; ++i) *chunk(buf, 4 * (J & 1) + i) = make_uint4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncthreads();
+            if (t0 + kSuTok <= it.t1) {
+                if (issuer && elect_one()) {
+                    su_tma_store(my, sb + kSuX, p0, h, t0);
+                    su_tma_store(my, sb + kSuC0, p0 + 32, h, t0);
+                    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                }
+            } else {  // not the rows of the next request: row by row
+#pragma unroll 1
+                for (int i = 0; i < 4; ++i) {
+                    const int r = 32 * i + 2 * warp + (lane >> 4), j = lane & 15;
+                    const uint4 v = *reinterpret_cast<const uint4*>(smem + (j < 8 ? kSuX : kSuC0) + r * 128 +
+                                                                    16 * ((j & 7) ^ (r & 7)));
+                    if (t0 + r < it.t1 && p0 + 4 * j < P)
+                        *reinterpret_cast<uint4*>(a.y + (static_cast<size_t>(t0 + r) * H + h) * P + p0 + 4 * j) = v;
                 }
             }
         }
+        if (issuer) {
+            if (more && elect_one()) {
+                mbar_expect_tx(bar_in, in_bytes);
+                load_x(t0 + kSuTok);
+                if (OUT) load_c0(t0 + kSuTok);
+            }
+            __syncwarp();
+        }
         if (!mbar_wait_bounded(bar_u, par, kWaitNs)) timed_out = true;
         su_fence_after();
-        if (tid == 0 && more) load_bc(t0 + kSuTok);  // U has read B and the parts of w x
+        if (issuer) {
+            if (more && elect_one()) load_bc(t0 + kSuTok);  // U has read B and the parts of w x
+            __syncwarp();
+        }
         const float dec = su_exp2(A2 * total);
         const float2 dec2 = make_float2(dec, dec);
         dtsum += total;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < 2; ++j) {
             uint32_t u0[8], u1[8], u2[8];
-            su_ld8(tml + kTmS + 32 * half + 8 * j, u0);
-            su_ld8(tml + kTmS + 64 + 32 * half + 8 * j, u1);
-            su_ld8(tml + kTmS + 128 + 32 * half + 8 * j, u2);
+            su_ld8(tml + kTmS + 16 * J + 8 * j, u0);
+            su_ld8(tml + kTmS + 64 + 16 * J + 8 * j, u1);
+            su_ld8(tml + kTmS + 128 + 16 * J + 8 * j, u2);
             su_wait_ld();
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -742,11 +794,11 @@ __global__ void __launch_bounds__(256, 2)
     }
     if (timed_out) set_error(a.err, RSSM_DEVERR_TIMEOUT);
     if ((!OUT || it.last) && row < N) {
-        float* out = OUT ? head_state(a, it.b, h) : slot_state(a, it.slot, h);
+        float* out = (OUT ? head_state(a, it.b, h) : slot_state(a, it.slot, h)) + static_cast<size_t>(pb) * N + row;
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            if (pb + 2 * j < P) out[static_cast<size_t>(pb + 2 * j) * N + row] = hst[j].x;
-            if (pb + 2 * j + 1 < P) out[static_cast<size_t>(pb + 2 * j + 1) * N + row] = hst[j].y;
+        for (int j = 0; j < 8; ++j) {
+            if (pb + 2 * j < P) out[2 * j * N] = hst[j].x;
+            if (pb + 2 * j + 1 < P) out[(2 * j + 1) * N] = hst[j].y;
         }
     }
     if (!OUT && tid == 0 && p0 == 0) *slot_dtsum(a, it.slot, h) = dtsum;
@@ -820,19 +872,31 @@ bool encode_rows(CUtensorMap* m, const void* base, int total, long long width) {
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// y [total][H][P] fp32, written in boxes of 128 tokens x 32 columns of a head.
+bool encode_out(CUtensorMap* m, float* base, int total, int H, int P) {
+    EncodeTiled fn = encode_tiled();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(P), static_cast<cuuint64_t>(H), static_cast<cuuint64_t>(total)};
+    const cuuint64_t strides[2] = {4ull * P, 4ull * P * H};
+    const cuuint32_t box[3] = {32, 1, kSuTok}, es[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, base, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <bool OUT>
 cudaError_t launch_umma(const ScanArgs& a, int items, cudaStream_t st) {
     const int slices = (a.s.P + 63) / 64;
-    CUtensorMap mx, mb, mc;
+    CUtensorMap mx, mb, mc, my;
     const long long xw = static_cast<long long>(a.s.H) * a.s.P, bw = static_cast<long long>(a.s.G) * a.s.N;
     if (!encode_rows(&mx, a.x, a.total, xw) || !encode_rows(&mb, a.B, a.total, bw) ||
-        !encode_rows(&mc, a.C, a.total, bw))
+        !encode_rows(&mc, a.C, a.total, bw) || !encode_out(&my, a.y, a.total, a.s.H, a.s.P))
         return cudaErrorInvalidValue;
     cudaError_t e = cudaFuncSetAttribute(k_scan_umma<OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(kSuSmem));
     if (e != cudaSuccess) return e;
     const dim3 grid(static_cast<unsigned>(items) * static_cast<unsigned>(a.s.H) * static_cast<unsigned>(slices));
-    k_scan_umma<OUT><<<grid, 256, kSuSmem, st>>>(a, mx, mb, mc, slices);
+    k_scan_umma<OUT><<<grid, kSuThreads, kSuSmem, st>>>(a, mx, mb, mc, my, slices);
     return cudaGetLastError();
 }
 
