@@ -210,10 +210,10 @@ __global__ void __launch_bounds__(kThreads) k_scan(const ScanArgs a) {
 // next block is fetched (TMA) as soon as its buffer has been read. Rows past
 // the request's end are zeroed in x and B.
 //
-// Decays. No difference of two long sums is formed: within a 32-token block
-// the exponent of M is a running sum of dt from s + 1 to t, and across
-// blocks M's factor is (start of t's block .. t) x (blocks between) x (s + 1
-// .. end of s's block), each the exponential of a sum of positive terms.
+// Decays. No difference of two sums of dt is formed: between two tokens of
+// the same 8 the exponent of M is the running sum of dt from s + 1 to t, and
+// else M's factor is (end of s's 8 tokens .. t) x (s + 1 .. end of s's 8
+// tokens), each the exponential of a sum of terms of one sign.
 //
 // Precision: a product of bf16 factors is exact in the fp32 sum. In two
 // parts everywhere, an output of a 512-token prompt was 1e-4 of the rms off
@@ -227,17 +227,17 @@ __global__ void __launch_bounds__(kThreads) k_scan(const ScanArgs a) {
 // output before them changes.
 // ---------------------------------------------------------------------------
 constexpr int kSuTok = 128;                    // tokens per block
-constexpr int kSuThreads = 512;
-constexpr int kSuIssuer = 12;                  // a warp with none of M's lower triangle
+constexpr int kSuThreads = 256;
+constexpr int kSuIssuer = 4;                   // a warp with none of M's lower triangle
 constexpr uint32_t kSuBlk = kSuTok * 128u;     // 128 rows of 128 bytes, swizzled: 16 KB
 constexpr uint32_t kSuB = 0;                   // B rows, two 64-column blocks
 constexpr uint32_t kSuX = 2 * kSuBlk;          // x rows
 constexpr uint32_t kSuR = 3 * kSuBlk;          // parts of h (2) or w x (hi, mid)
 constexpr uint32_t kSuC1 = 5 * kSuBlk;         // C columns 64.. ; later w x lo (right behind hi, mid)
 constexpr uint32_t kSuC0 = 6 * kSuBlk;         // C columns 0..63
-constexpr uint32_t kSuCol = 7 * kSuBlk;        // float [128]: dt_s exp(decay from s + 1 to its 32-block's end)
-constexpr uint32_t kSuSum = kSuCol + 512;      // float [4]: dt sums of the 32-blocks
-constexpr uint32_t kSuBar = kSuSum + 16;       // 5 mbarriers, tensor-memory address
+constexpr uint32_t kSuCol = 7 * kSuBlk;        // float [128]: dt_s exp(decay from s + 1 to the end of its 8 tokens)
+constexpr uint32_t kSuSum = kSuCol + 512;      // float [16]: dt sums of 8 tokens each
+constexpr uint32_t kSuBar = kSuSum + 64;       // 5 mbarriers, tensor-memory address
 constexpr uint32_t kSuSmem = kSuBar + 48;
 constexpr uint32_t kSuCols = 256;              // tensor-memory columns
 constexpr uint32_t kTmS = 0, kTmLo = 128, kTmY = 192;  // S, then M hi, mid; M lo; O, then Y (U: 0..191)
@@ -392,6 +392,11 @@ __device__ __forceinline__ void su_tma_store(const CUtensorMap& map, uint32_t sr
                  : "memory");
 }
 
+// The same box into L2 only.
+__device__ __forceinline__ void su_prefetch(const CUtensorMap& map, int x, int y) {
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global [%0, {%1, %2}];" ::"l"(&map), "r"(x), "r"(y) : "memory");
+}
+
 template <bool OUT>
 __global__ void __launch_bounds__(kSuThreads, 2)
     k_scan_umma(const ScanArgs a, const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mb,
@@ -403,7 +408,7 @@ __global__ void __launch_bounds__(kSuThreads, 2)
     if (!find_item<OUT>(a, blockIdx.x / (H * slices), it)) return;
     const int g = h / (H / G), tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
-    const int q = warp & 3, J = warp >> 2;  // rows 32 q .., 32-block J of M's columns, columns 16 J .. elsewhere
+    const int q = warp & 3, half = warp >> 2;  // rows 32 q .., half the columns
     const int row = 32 * q + lane;          // this thread's token and state row
     const uint32_t sb = smem_u32(smem);
     if (sb & 1023u) {  // the swizzled operands lie on 1024-byte boundaries
@@ -444,13 +449,13 @@ __global__ void __launch_bounds__(kSuThreads, 2)
     const float A2 = a.A[h] * 1.4426950408889634f < -3e38f ? -3e38f : a.A[h] * 1.4426950408889634f;
     const float Dh = OUT ? a.D[h] : 0.f;
 
-    // the state: row `row` (d_state), columns 16 J .. + 15 of the head_dim slice
-    float2 hst[8];
+    // the state: row `row` (d_state), columns 32 half .. + 31 of the head_dim slice
+    float2 hst[16];
     const float* init = it.slot < 0 ? head_state(a, it.b, h) : slot_state(a, it.slot, h);
-    const int pb = p0 + 16 * J;  // this thread's first column
+    const int pb = p0 + 32 * half;  // this thread's first column
     auto init_at = [&](int j) { return OUT && row < N && pb + j < P ? init[static_cast<size_t>(pb + j) * N + row] : 0.f; };
 #pragma unroll
-    for (int j = 0; j < 8; ++j) hst[j] = make_float2(init_at(2 * j), init_at(2 * j + 1));
+    for (int j = 0; j < 16; ++j) hst[j] = make_float2(init_at(2 * j), init_at(2 * j + 1));
 
     // 16-byte chunk j of this thread's row in a buffer
     auto chunk = [&](uint32_t buf, int j) {
@@ -458,33 +463,34 @@ __global__ void __launch_bounds__(kSuThreads, 2)
     };
     auto put_state = [&]() {  // hi and lo parts of the state, d_state row by row
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+        for (int j = 0; j < 4; ++j) {
             uint32_t hi[4], lo[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 hi[i] = pack_bf16(hst[4 * j + i]);
                 lo[i] = pack_bf16(sub2(hst[4 * j + i], bf2(hi[i])));
             }
-            *chunk(kSuR, 2 * J + j) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *chunk(kSuR + kSuBlk, 2 * J + j) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            *chunk(kSuR, 4 * half + j) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *chunk(kSuR + kSuBlk, 4 * half + j) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
     };
-    // decays of this thread's token within its 32-block, from d
+    // decays of this thread's token within its group of 8, from d
     float* s_col = reinterpret_cast<float*>(smem + kSuCol);
-    float rowf;
+    const int oct = lane >> 3;
+    float pre;  // dt sum from the group's start to the token
     auto scan_dt = [&]() {
-        float pre = d, suf = d;  // inclusive sums from the 32-block's start, to its end
+        float suf = d;  // to the group's end
+        pre = d;
 #pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const float u = __shfl_up_sync(0xffffffffu, pre, off), v = __shfl_down_sync(0xffffffffu, suf, off);
-            if (lane >= off) pre += u;
-            if (lane + off < 32) suf += v;
+        for (int off = 1; off < 8; off <<= 1) {
+            const float u = __shfl_up_sync(0xffffffffu, pre, off, 8), v = __shfl_down_sync(0xffffffffu, suf, off, 8);
+            if ((lane & 7) >= off) pre += u;
+            if ((lane & 7) + off < 8) suf += v;
         }
-        const float next = __shfl_down_sync(0xffffffffu, suf, 1);
-        rowf = su_exp2(A2 * pre);
-        if (J == 0) {
-            s_col[row] = d * su_exp2(A2 * (lane == 31 ? 0.f : next));
-            if (lane == 0) reinterpret_cast<float*>(smem + kSuSum)[q] = suf;
+        const float next = __shfl_down_sync(0xffffffffu, suf, 1, 8);
+        if (half == 0) {
+            s_col[row] = d * su_exp2(A2 * ((lane & 7) == 7 ? 0.f : next));
+            if ((lane & 7) == 0) reinterpret_cast<float*>(smem + kSuSum)[4 * q + oct] = suf;
         }
     };
     if (OUT) put_state();
@@ -505,10 +511,10 @@ __global__ void __launch_bounds__(kSuThreads, 2)
         if (!more && t0 + row >= it.t1) {  // rows of the next request, or of none
             const uint4 zero = make_uint4(0, 0, 0, 0);
 #pragma unroll
-            for (int j = 0; j < 2; ++j) *chunk(kSuX, 2 * J + j) = zero;
-            if (wide || J < 2)
+            for (int j = 0; j < 4; ++j) *chunk(kSuX, 4 * half + j) = zero;
+            if (wide || half == 0)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) *chunk(kSuB + (J >> 1) * kSuBlk, 4 * (J & 1) + j) = zero;
+                for (int j = 0; j < 8; ++j) *chunk(kSuB + half * kSuBlk, j) = zero;
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         su_fence_before();
@@ -532,10 +538,13 @@ __global__ void __launch_bounds__(kSuThreads, 2)
                         su_mma<su_idesc(64, 0, 1)>(tm + kTmY, c, dR + kSuBlk / 16 + 128 * ks, 1);
                     }
                 su_commit(bar_o);
+                if (more) su_prefetch(mx, xx, t0 + kSuTok);
             }
             __syncwarp();
         }
-        const float4 sums = *reinterpret_cast<const float4*>(smem + kSuSum);  // of the 32-blocks' dt
+        const float4* s_sum = reinterpret_cast<const float4*>(smem + kSuSum);
+        auto sum4 = [&](int i) { return (s_sum[i].x + s_sum[i].y) + (s_sum[i].z + s_sum[i].w); };
+        const float4 sums = make_float4(sum4(0), sum4(1), sum4(2), sum4(3));  // of the 32-blocks' dt
         const float total = sums.x + sums.y + sums.z + sums.w;
 
         // chunk j of x of this block's token s, as given
@@ -545,59 +554,87 @@ __global__ void __launch_bounds__(kSuThreads, 2)
                                                    (static_cast<size_t>(t0 + s) * H + h) * P + p0 + 8 * j);
         };
         if (OUT) {
-            // dt sums of the 32-blocks before this thread's token's, and between J and it
+            // dt sums from the start of this thread's token's 32-block to the token,
+            // of the 32-blocks before, and of those between J and it
+            const float4 mine = s_sum[q];
+            const float pre32 = pre + ((oct > 0 ? mine.x : 0.f) + (oct > 1 ? mine.y : 0.f) + (oct > 2 ? mine.z : 0.f));
             const float before = (q > 0 ? sums.x : 0.f) + (q > 1 ? sums.y : 0.f) + (q > 2 ? sums.z : 0.f);
-            const float between = (J < 1 && q > 1 ? sums.y : 0.f) + (J < 2 && q > 2 ? sums.z : 0.f);
-            const float rb = rowf * su_exp2(A2 * between);
+            // the same 8 tokens' factors, from the running sum: A2 times the dt sum from s + 1 to t
+            float own[8];
+            if ((q >> 1) == half) {
+                float run = 0.f, dnx = 0.f;
+#pragma unroll
+                for (int j = 7; j >= 0; --j) {
+                    const float ds = __shfl_sync(0xffffffffu, d, j, 8);
+                    if ((lane & 7) > j) run = fmaf(A2, dnx, run);
+                    dnx = ds;
+                    own[j] = ds * su_exp2(run);
+                }
+            }
             if (!mbar_wait_bounded(bar_s, par, kWaitNs)) timed_out = true;
             su_fence_after();
-            // M over S, 32-block J of its columns, 16 at a time: hi and mid parts
-            // in the columns read, lo in its own
-            const uint32_t tS = tml + kTmS + 32 * J, tL = tml + kTmLo + 16 * J;
-            if (J > q) {  // nothing but later tokens
-                const uint32_t zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+            // M over S, 32-blocks 2 half and 2 half + 1 of its columns, 16 at a
+            // time: hi and mid parts in the columns read, lo in its own
+#pragma unroll 1
+            for (int J = 2 * half; J < 2 * half + 2; ++J) {
+                const uint32_t tS = tml + kTmS + 32 * J, tL = tml + kTmLo + 16 * J;
+                if (J > q) {  // nothing but later tokens
+                    const uint32_t zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        su_st8(tS + 16 * k, zero);
+                        su_st8(tS + 16 * k + 8, zero);
+                        su_st8(tL + 8 * k, zero);
+                    }
+                    continue;
+                }
+                // decay from the end of each 8 tokens of the columns to this thread's token
+                const float4 o = s_sum[J];
+                float to = pre32;  // from the end of the 32-block
+                if (J == q) to = pre;
+                if (J < 1 && q > 1) to += sums.y;
+                if (J < 2 && q > 2) to += sums.z;
+                float f[4];
+                if (J == q) {  // (of columns of its own 8 tokens or later ones: not used)
+                    f[0] = su_exp2(A2 * (to + ((oct > 1 ? o.y : 0.f) + (oct > 2 ? o.z : 0.f))));
+                    f[1] = su_exp2(A2 * (to + (oct > 2 ? o.z : 0.f)));
+                    f[2] = su_exp2(A2 * to);
+                    f[3] = 0.f;
+                } else {
+                    f[3] = su_exp2(A2 * to);
+                    f[2] = su_exp2(A2 * (to + o.w));
+                    f[1] = su_exp2(A2 * (to + (o.z + o.w)));
+                    f[0] = su_exp2(A2 * (to + (o.y + o.z + o.w)));
+                }
+                const float4* c4 = reinterpret_cast<const float4*>(s_col + 32 * J);
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    su_st8(tS + 16 * k, zero);
-                    su_st8(tS + 16 * k + 8, zero);
-                    su_st8(tL + 8 * k, zero);
-                }
-            } else {
-                const float2 rb2 = make_float2(rb, rb);
-                float run = 0.f;   // A2 times the dt sum from s + 1 to t
-                float dnx = 0.f;   // dt of s + 1
-#pragma unroll 1
-                for (int k = 1; k >= 0; --k) {
                     uint32_t v[16];
                     su_ld16(tS + 16 * k, v);
                     float2 m[8];
-                    if (J == q) {
-                        su_wait_ld();
 #pragma unroll
-                        for (int i = 15; i >= 0; --i) {
-                            const int s = 16 * k + i;
-                            const float ds = __shfl_sync(0xffffffffu, d, s);
-                            if (lane > s) run = fmaf(A2, dnx, run);
-                            dnx = ds;
-                            const float f = ds * su_exp2(run);
-                            float e = lane >= s ? __uint_as_float(v[i]) * f : 0.f;
-                            if (lane == s) e += Dh;  // D x_t
-                            if (i & 1)
-                                m[i / 2].y = e;
-                            else
-                                m[i / 2].x = e;
+                    for (int i = 0; i < 4; ++i) {
+                        const float4 c = c4[4 * k + i];
+                        const float2 f2 = make_float2(f[2 * k + i / 2], f[2 * k + i / 2]);
+                        m[2 * i] = mul2(f2, make_float2(c.x, c.y));
+                        m[2 * i + 1] = mul2(f2, make_float2(c.z, c.w));
+                    }
+                    su_wait_ld();
+                    if (J == q) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int c = 16 * k + 2 * i;
+                            float2 w = m[i];
+                            if (oct == (c >> 3)) w = make_float2(own[c & 7], own[(c & 7) + 1]);
+                            m[i].x = lane >= c ? __uint_as_float(v[2 * i]) * w.x : 0.f;
+                            m[i].y = lane > c ? __uint_as_float(v[2 * i + 1]) * w.y : 0.f;
+                            if (lane == c) m[i].x += Dh;  // D x_t
+                            if (lane == c + 1) m[i].y += Dh;
                         }
                     } else {
-                        const float4* c4 = reinterpret_cast<const float4*>(s_col + 32 * J + 16 * k);
-                        su_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float4 c = c4[i];
-                            m[2 * i] = mul2(make_float2(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1])),
-                                            mul2(rb2, make_float2(c.x, c.y)));
-                            m[2 * i + 1] = mul2(make_float2(__uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3])),
-                                                mul2(rb2, make_float2(c.z, c.w)));
-                        }
+                        for (int i = 0; i < 8; ++i)
+                            m[i] = mul2(m[i], make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])));
                     }
                     uint32_t hi[8], mid[8], lo[8];
 #pragma unroll
@@ -608,36 +645,44 @@ __global__ void __launch_bounds__(kSuThreads, 2)
                 }
             }
             // the state's share of the outputs, scaled in place; Y is added to it
-            const float fac = rowf * su_exp2(A2 * before);
+            const float fac = su_exp2(A2 * (before + pre32));
             const float2 fac2 = make_float2(fac, fac);
             if (!mbar_wait_bounded(bar_o, par, kWaitNs)) timed_out = true;
             su_fence_after();
             {
-                uint32_t o[16];
-                su_ld16(tml + kTmY + 16 * J, o);
+                uint32_t o[2][16];
+                su_ld16(tml + kTmY + 32 * half, o[0]);
+                su_ld16(tml + kTmY + 32 * half + 16, o[1]);
                 su_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float2 v = mul2(fac2, make_float2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1])));
-                    o[2 * i] = __float_as_uint(v.x);
-                    o[2 * i + 1] = __float_as_uint(v.y);
+                for (int j = 0; j < 2; ++j) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float2 v =
+                            mul2(fac2, make_float2(__uint_as_float(o[j][2 * i]), __uint_as_float(o[j][2 * i + 1])));
+                        o[j][2 * i] = __float_as_uint(v.x);
+                        o[j][2 * i + 1] = __float_as_uint(v.y);
+                    }
+                    su_st16(tml + kTmY + 32 * half + 16 * j, o[j]);
                 }
-                su_st16(tml + kTmY + 16 * J, o);
             }
             su_wait_st();
         }
         // w x in three parts. The warps of rows 32 q .. have the more of M the
-        // larger q: those of q = 0 take 3 of the 8 passes over 16 token rows,
-        // the others 2, 2 and 1, a 16-byte chunk per thread and pass.
+        // larger q: those of q = 0 take 6 of the 16 passes over 8 token rows,
+        // the others 4, 4 and 2, a 16-byte chunk per thread and pass.
         const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
         __nv_bfloat162 z = zero;  // NaN when x has a NaN or infinity
-#pragma unroll 1
-        for (int pass = q == 0 ? 0 : 2 * q + 1, end = q == 3 ? 8 : 2 * q + 3; pass < end; ++pass) {
-            const int s = 16 * pass + 4 * J + (lane >> 3);
+#pragma unroll 2
+        for (int pass = q == 0 ? 0 : 4 * q + 2, end = q == 3 ? 16 : 4 * q + 6; pass < end; ++pass) {
+            const int s = 8 * pass + 4 * half + (lane >> 3);
             const uint32_t at = static_cast<uint32_t>(128 * s + 16 * ((lane & 7) ^ (s & 7)));
             const uint4 u = *reinterpret_cast<const uint4*>(smem + kSuX + at);
-            // dt sum of the 32-blocks after the token's
-            const float after = (pass < 2 ? sums.y : 0.f) + (pass < 4 ? sums.z : 0.f) + (pass < 6 ? sums.w : 0.f);
+            // dt sums of the groups of 8 after the token's in its 32-block, and of the 32-blocks after
+            const float4 o = s_sum[pass >> 2];
+            const int so = pass & 3;
+            const float after = ((so < 1 ? o.y : 0.f) + (so < 2 ? o.z : 0.f) + (so < 3 ? o.w : 0.f)) +
+                                ((pass < 4 ? sums.y : 0.f) + (pass < 8 ? sums.z : 0.f) + (pass < 12 ? sums.w : 0.f));
             const float w = s_col[s] * su_exp2(A2 * after);
             const float2 w2 = make_float2(w, w);
             const uint32_t xu[4] = {u.x, u.y, u.z, u.w};
@@ -657,8 +702,8 @@ __global__ void __launch_bounds__(kSuThreads, 2)
         const bool bad = __syncthreads_or(OUT && (__hisnan(z.x) || __hisnan(z.y)));
         if (OUT && bad) {
 #pragma unroll 1
-            for (int j = 0; j < 2; ++j) {
-                uint4* c = chunk(kSuX, 2 * J + j);
+            for (int j = 0; j < 4; ++j) {
+                uint4* c = chunk(kSuX, 4 * half + j);
                 const uint4 u = *c;
                 *c = make_uint4(finite2(u.x), finite2(u.y), finite2(u.z), finite2(u.w));
             }
@@ -689,7 +734,7 @@ __global__ void __launch_bounds__(kSuThreads, 2)
         }
         if (OUT && bad) {  // what was left out of Y, 8 columns at a time, before U takes M's place
 #pragma unroll 1
-            for (int j = 0; j < 2; ++j) {
+            for (int j = 0; j < 4; ++j) {
                 float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll 1
                 for (int s = 0; s < kSuTok; ++s) {
@@ -699,7 +744,7 @@ __global__ void __launch_bounds__(kSuThreads, 2)
                     su_ld1(tml + kTmLo + (s >> 1), lo);
                     su_wait_ld();
                     const float m = s & 1 ? bf_hi(hi) + (bf_hi(mid) + bf_hi(lo)) : bf_lo(hi) + (bf_lo(mid) + bf_lo(lo));
-                    const uint4 u = x_given(s, 2 * J + j);
+                    const uint4 u = x_given(s, 4 * half + j);
                     const uint32_t xu[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
@@ -709,11 +754,11 @@ __global__ void __launch_bounds__(kSuThreads, 2)
                     }
                 }
                 uint32_t y[8];
-                su_ld8(tml + kTmY + 16 * J + 8 * j, y);
+                su_ld8(tml + kTmY + 32 * half + 8 * j, y);
                 su_wait_ld();
 #pragma unroll
                 for (int i = 0; i < 8; ++i) y[i] = __float_as_uint(__uint_as_float(y[i]) + acc[i]);
-                su_st8(tml + kTmY + 16 * J + 8 * j, y);
+                su_st8(tml + kTmY + 32 * half + 8 * j, y);
             }
             su_wait_st();
             su_fence_before();
@@ -732,12 +777,16 @@ __global__ void __launch_bounds__(kSuThreads, 2)
         }
         if (OUT) {
             // Y by way of the buffers of x and C's first half, 32 columns each
-            uint32_t y[16];
-            su_ld16(tml + kTmY + 16 * J, y);
+            uint32_t y[2][16];
+            su_ld16(tml + kTmY + 32 * half, y[0]);
+            su_ld16(tml + kTmY + 32 * half + 16, y[1]);
             su_wait_ld();
-            const uint32_t buf = J < 2 ? kSuX : kSuC0;
+            const uint32_t buf = half ? kSuC0 : kSuX;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) *chunk(buf, 4 * (J & 1) + i) = make_uint4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t* v = &y[i >> 2][4 * (i & 3)];
+                *chunk(buf, i) = make_uint4(v[0], v[1], v[2], v[3]);
+            }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncthreads();
             if (t0 + kSuTok <= it.t1) {
@@ -749,8 +798,8 @@ __global__ void __launch_bounds__(kSuThreads, 2)
                 }
             } else {  // not the rows of the next request: row by row
 #pragma unroll 1
-                for (int i = 0; i < 4; ++i) {
-                    const int r = 32 * i + 2 * warp + (lane >> 4), j = lane & 15;
+                for (int i = 0; i < 8; ++i) {
+                    const int r = 16 * i + 2 * warp + (lane >> 4), j = lane & 15;
                     const uint4 v = *reinterpret_cast<const uint4*>(smem + (j < 8 ? kSuX : kSuC0) + r * 128 +
                                                                     16 * ((j & 7) ^ (r & 7)));
                     if (t0 + r < it.t1 && p0 + 4 * j < P)
@@ -776,11 +825,11 @@ __global__ void __launch_bounds__(kSuThreads, 2)
         const float2 dec2 = make_float2(dec, dec);
         dtsum += total;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+        for (int j = 0; j < 4; ++j) {
             uint32_t u0[8], u1[8], u2[8];
-            su_ld8(tml + kTmS + 16 * J + 8 * j, u0);
-            su_ld8(tml + kTmS + 64 + 16 * J + 8 * j, u1);
-            su_ld8(tml + kTmS + 128 + 16 * J + 8 * j, u2);
+            su_ld8(tml + kTmS + 32 * half + 8 * j, u0);
+            su_ld8(tml + kTmS + 64 + 32 * half + 8 * j, u1);
+            su_ld8(tml + kTmS + 128 + 32 * half + 8 * j, u2);
             su_wait_ld();
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -796,7 +845,7 @@ __global__ void __launch_bounds__(kSuThreads, 2)
     if ((!OUT || it.last) && row < N) {
         float* out = (OUT ? head_state(a, it.b, h) : slot_state(a, it.slot, h)) + static_cast<size_t>(pb) * N + row;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < 16; ++j) {
             if (pb + 2 * j < P) out[2 * j * N] = hst[j].x;
             if (pb + 2 * j + 1 < P) out[(2 * j + 1) * N] = hst[j].y;
         }
