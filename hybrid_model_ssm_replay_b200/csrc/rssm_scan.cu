@@ -538,7 +538,13 @@ __global__ void __launch_bounds__(kSuThreads, 2)
                         su_mma<su_idesc(64, 0, 1)>(tm + kTmY, c, dR + kSuBlk / 16 + 128 * ks, 1);
                     }
                 su_commit(bar_o);
-                if (more) su_prefetch(mx, xx, t0 + kSuTok);
+                if (more) {  // the next block on its way to L2
+                    su_prefetch(mx, xx, t0 + kSuTok);
+                    su_prefetch(mb, bx, t0 + kSuTok);
+                    su_prefetch(mc, bx, t0 + kSuTok);
+                    if (wide) su_prefetch(mb, bx + 64, t0 + kSuTok);
+                    if (wide) su_prefetch(mc, bx + 64, t0 + kSuTok);
+                }
             }
             __syncwarp();
         }
@@ -607,10 +613,12 @@ __global__ void __launch_bounds__(kSuThreads, 2)
                     f[0] = su_exp2(A2 * (to + (o.y + o.z + o.w)));
                 }
                 const float4* c4 = reinterpret_cast<const float4*>(s_col + 32 * J);
+uint32_t vv[2][16];
+                    su_ld16(tS, vv[0]);
+                    su_ld16(tS + 16, vv[1]);
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    uint32_t v[16];
-                    su_ld16(tS + 16 * k, v);
+                    uint32_t (&v)[16] = vv[k];
                     float2 m[8];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
@@ -619,7 +627,7 @@ __global__ void __launch_bounds__(kSuThreads, 2)
                         m[2 * i] = mul2(f2, make_float2(c.x, c.y));
                         m[2 * i + 1] = mul2(f2, make_float2(c.z, c.w));
                     }
-                    su_wait_ld();
+                    if (k == 0) su_wait_ld();
                     if (J == q) {
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
@@ -668,21 +676,25 @@ __global__ void __launch_bounds__(kSuThreads, 2)
             }
             su_wait_st();
         }
-        // w x in three parts. The warps of rows 32 q .. have the more of M the
-        // larger q: those of q = 0 take 6 of the 16 passes over 8 token rows,
-        // the others 4, 4 and 2, a 16-byte chunk per thread and pass.
+        // w x in three parts, 32 passes over 4 token rows, a 16-byte chunk per
+        // thread and pass. With M to build, a warp has 0, 1 or 2 of its 32 x 32
+        // blocks, the diagonal ones dearer: the passes even that out among the
+        // warps, and among the four warps of each q, which share a scheduler.
         const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
         __nv_bfloat162 z = zero;  // NaN when x has a NaN or infinity
-#pragma unroll 2
-        for (int pass = q == 0 ? 0 : 4 * q + 2, end = q == 3 ? 16 : 4 * q + 6; pass < end; ++pass) {
-            const int s = 8 * pass + 4 * half + (lane >> 3);
+        constexpr uint64_t kFirst = OUT ? 0x1F180D041C160C00ull : 0x1C1814100C080400ull;  // byte w: warp w's first pass
+        constexpr uint32_t kPasses = OUT ? 0x14983214u : 0x44444444u;                      // digit w: how many
+        const int first = static_cast<int>((kFirst >> (8 * warp)) & 31), passes = (kPasses >> (4 * warp)) & 15;
+#pragma unroll 1
+        for (int pass = first; pass < first + passes; ++pass) {
+            const int s = 4 * pass + (lane >> 3);
             const uint32_t at = static_cast<uint32_t>(128 * s + 16 * ((lane & 7) ^ (s & 7)));
             const uint4 u = *reinterpret_cast<const uint4*>(smem + kSuX + at);
             // dt sums of the groups of 8 after the token's in its 32-block, and of the 32-blocks after
-            const float4 o = s_sum[pass >> 2];
-            const int so = pass & 3;
+            const float4 o = s_sum[pass >> 3];
+            const int so = (pass >> 1) & 3;
             const float after = ((so < 1 ? o.y : 0.f) + (so < 2 ? o.z : 0.f) + (so < 3 ? o.w : 0.f)) +
-                                ((pass < 4 ? sums.y : 0.f) + (pass < 8 ? sums.z : 0.f) + (pass < 12 ? sums.w : 0.f));
+                                ((pass < 8 ? sums.y : 0.f) + (pass < 16 ? sums.z : 0.f) + (pass < 24 ? sums.w : 0.f));
             const float w = s_col[s] * su_exp2(A2 * after);
             const float2 w2 = make_float2(w, w);
             const uint32_t xu[4] = {u.x, u.y, u.z, u.w};
@@ -825,18 +837,18 @@ __global__ void __launch_bounds__(kSuThreads, 2)
         const float2 dec2 = make_float2(dec, dec);
         dtsum += total;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            uint32_t u0[8], u1[8], u2[8];
-            su_ld8(tml + kTmS + 32 * half + 8 * j, u0);
-            su_ld8(tml + kTmS + 64 + 32 * half + 8 * j, u1);
-            su_ld8(tml + kTmS + 128 + 32 * half + 8 * j, u2);
+        for (int j = 0; j < 2; ++j) {
+            uint32_t u0[16], u1[16], u2[16];
+            su_ld16(tml + kTmS + 32 * half + 16 * j, u0);
+            su_ld16(tml + kTmS + 64 + 32 * half + 16 * j, u1);
+            su_ld16(tml + kTmS + 128 + 32 * half + 16 * j, u2);
             su_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                auto two = [&](const uint32_t (&u)[8]) {
+            for (int i = 0; i < 8; ++i) {
+                auto two = [&](const uint32_t (&u)[16]) {
                     return make_float2(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]));
                 };
-                hst[4 * j + i] = fma2(dec2, hst[4 * j + i], add2(two(u0), add2(two(u1), two(u2))));
+                hst[8 * j + i] = fma2(dec2, hst[8 * j + i], add2(two(u0), add2(two(u1), two(u2))));
             }
         }
         if (OUT && more) put_state();
