@@ -2,6 +2,7 @@
 // over packed prompts (include/rssm_stage.h): the causal conv1d + SiLU with
 // the dt softplus and the conv state, the gated RMS norm, and the residual
 // add with the norms around it. All are bound by the bytes they move.
+#include <atomic>
 #include <cmath>
 #include <initializer_list>
 
@@ -15,10 +16,26 @@ namespace {
 
 constexpr int kTaps = RSSM_STAGE_CONV_WIDTH;  // 4: three past inputs + the current one
 constexpr int kConvThreads = 256;
-constexpr int kConvTok = 16;    // tokens per CTA
 constexpr int kNormThreads = 256;
 
 __device__ __forceinline__ float bf(const __nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    uint32_t d;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+__device__ __forceinline__ float ex2_approx(float v) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ float rcp_approx(float v) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
 
 __device__ __forceinline__ void set_error(int32_t* err, int32_t code) {
     if (err) atomicCAS(err, 0, code);
@@ -26,6 +43,7 @@ __device__ __forceinline__ void set_error(int32_t* err, int32_t code) {
 
 struct ConvPromptArgs {
     int batch, total, din, gn, H;
+    int tok;     // tokens per CTA
     const int32_t* cu;
     const __nv_bfloat16* zx;
     __nv_bfloat16* state;
@@ -39,49 +57,104 @@ struct ConvPromptArgs {
     int32_t* err;
 };
 
+// silu as rssm_stage_conv forms it, in bf16.
+__device__ __noinline__ __nv_bfloat16 silu_exact(float o) { return __float2bfloat16_rn(o / (1.0f + expf(-o))); }
+
+// The same bits for less: o rcp(1 + 2^(-o log2 e)) from the approximate
+// instructions is, for |o| < 32, within 23 fp32 spacings of the quotient (19
+// from the argument -o log2 e, up to 46 in size, 2 of ex2, 1 of rcp, 1 of the
+// add and the product) and the library form within 3, so both round to the
+// same bf16 unless the value lies within 32 spacings of the middle between
+// two bf16 (one value in a thousand), which take the library form.
+__device__ __forceinline__ float silu_fast(float o, bool& sure) {
+    const float v = o * rcp_approx(1.0f + ex2_approx(o * -1.4426950408889634f));
+    const uint32_t off = (__float_as_uint(v) - (0x8000u - 32u)) & 0xFFFFu;
+    sure = off > 64u && fabsf(o) < 32.0f && fabsf(v) > 1e-30f;
+    return v;
+}
+
+template <int VEC> struct Chans;  // VEC consecutive channels as they are kept
+template <> struct Chans<8> {
+    uint4 u;
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = *reinterpret_cast<const uint4*>(p); }
+    __device__ __forceinline__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = u; }
+    __device__ __forceinline__ float get(int i) const {
+        const uint32_t w = i < 2 ? u.x : i < 4 ? u.y : i < 6 ? u.z : u.w;
+        return i & 1 ? bf_hi(w) : bf_lo(w);
+    }
+};
+template <> struct Chans<1> {
+    __nv_bfloat16 u;
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = *p; }
+    __device__ __forceinline__ void store(__nv_bfloat16* p) const { *p = u; }
+    __device__ __forceinline__ float get(int) const { return bf(u); }
+};
+
+// The first request that ends past token t: each lane tries a part of the range.
+__device__ __forceinline__ int first_request(const int32_t* cu, int batch, int t) {
+    const int lane = threadIdx.x & 31;
+    int lo = 0, hi = batch;
+    while (lo < hi) {
+        const int step = (hi - lo + 31) >> 5, r = lo + lane * step;
+        const unsigned past = __ballot_sync(0xffffffffu, r < hi && cu[r + 1] <= t);
+        const int n = __popc(past);
+        if (n == 0) break;
+        hi = min(hi, lo + n * step);
+        lo = lo + (n - 1) * step + 1;
+    }
+    return lo;
+}
+
 // ---------------------------------------------------------------------------
-// CTA (blockIdx.x, blockIdx.y): kConvTok tokens from kConvTok * blockIdx.x on,
-// 256 lanes of [x | B | C | dt], one lane per thread. A thread walks its
-// channel's tokens with the three inputs before the token in registers.
-// The conv state of a request is read and written by one CTA alone, the one
-// that holds the request's first token: it also runs the request's second
-// and third token, which read the old state too, when they lie past its own
-// tokens (the next CTA leaves them out), and it writes the state's new rows,
-// the request's last three inputs, from the projection's rows.
+// CTA (blockIdx.x, blockIdx.y): a.tok tokens from a.tok * blockIdx.x on, 256
+// threads of VEC channels of [x | B | C] each, the last blockIdx.y the dt
+// heads. A thread walks its channels' tokens with the three inputs before the
+// token in registers. The conv state of a request is read and written by one
+// CTA alone, the one that holds the request's first token: it also runs the
+// request's second and third token, which read the old state too, when they
+// lie past its own tokens (the next CTA leaves them out), and it writes the
+// state's new rows, the request's last three inputs, from the projection's
+// rows. Bound by the bytes: each input row is read once plus three rows of a
+// CTA's tokens before (from L2), each output written once; four rows are in
+// flight per thread. B200, 256 prompts of 512 tokens, 6144 channels (3.29 GB):
+// @CONV@.
 // ---------------------------------------------------------------------------
+template <int VEC>
 __global__ void __launch_bounds__(kConvThreads) k_conv_prompt(const ConvPromptArgs a) {
     const int chans = a.din + 2 * a.gn;
     const size_t Dp = static_cast<size_t>(a.din) + chans + a.H;
-    const int c = blockIdx.y * kConvThreads + threadIdx.x;
-    const int t0 = blockIdx.x * kConvTok, t1 = min(a.total - t0, kConvTok) + t0;
+    const int t0 = blockIdx.x * a.tok, t1 = min(a.total - t0, a.tok) + t0;
     if (blockIdx.x == 0 && blockIdx.y == 0)  // every range, those without a token here too
         for (int r = threadIdx.x; r < a.batch; r += kConvThreads)
             if (a.cu[r] < 0 || a.cu[r + 1] < a.cu[r] || a.cu[r + 1] > a.total) set_error(a.err, RSSM_DEVERR_SEQ_RANGE);
-    if (c >= chans + a.H) return;
-    // the first request that ends past t0
-    int lo = 0, hi = a.batch;
-    while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (a.cu[mid + 1] > t0)
-            hi = mid;
-        else
-            lo = mid + 1;
-    }
-    if (c >= chans) {  // dt
-        const int h = c - chans;
-        for (int r = lo; r < a.batch; ++r) {
+    const int request0 = first_request(a.cu, a.batch, t0);
+    if (blockIdx.y == gridDim.y - 1) {  // dt
+        for (int r = request0; r < a.batch; ++r) {
             const int s = a.cu[r], e = a.cu[r + 1];
             if (s >= t1) break;
             if (s < 0 || e < s || e > a.total) continue;
-            for (int t = max(s, t0); t < min(e, t1); ++t) {
+            const int from = max(s, t0), n = (min(e, t1) - from) * a.H;
+            for (int i = threadIdx.x; i < n; i += kConvThreads) {
+                const size_t t = from + i / a.H;
+                const int h = i % a.H;
                 const float v = bf(a.zx[t * Dp + a.din + chans + h]) + a.dt_bias[h];
-                a.dt[static_cast<size_t>(t) * a.H + h] = v > 20.0f ? v : log1pf(expf(v));
+                a.dt[t * a.H + h] = v > 20.0f ? v : log1pf(expf(v));
             }
         }
         return;
     }
-    const float4 w = reinterpret_cast<const float4*>(a.w)[c];
-    const float bias = a.bias[c];
+    const int c = VEC * (blockIdx.y * kConvThreads + threadIdx.x);
+    if (c >= chans) return;
+    float w[VEC][kTaps], bias[VEC];
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+        const float4 v = reinterpret_cast<const float4*>(a.w)[c + i];
+        w[i][0] = v.x;
+        w[i][1] = v.y;
+        w[i][2] = v.z;
+        w[i][3] = v.w;
+        bias[i] = a.bias[c + i];
+    }
     const __nv_bfloat16* in = a.zx + a.din + c;
     __nv_bfloat16* dst;
     int width;
@@ -95,67 +168,177 @@ __global__ void __launch_bounds__(kConvThreads) k_conv_prompt(const ConvPromptAr
         dst = a.C + (c - a.din - a.gn);
         width = a.gn;
     }
-    for (int r = lo; r < a.batch; ++r) {
+    for (int r = request0; r < a.batch; ++r) {
         const int s = a.cu[r], e = a.cu[r + 1];
         if (s >= t1) break;
         if (s < 0 || e <= s || e > a.total) continue;
         const bool first = s >= t0;
         const int from = first ? s : max(t0, s + kTaps - 1);
         const int to = first ? max(min(e, t1), min(e, s + kTaps - 1)) : min(e, t1);
-        __nv_bfloat16* st = a.state + static_cast<size_t>(r) * (kTaps - 1) * chans + c;
-        __nv_bfloat16 r0, r1, r2;
+        Chans<VEC> r0, r1, r2;
         if (first) {
-            r0 = st[0];
-            r1 = st[chans];
-            r2 = st[2 * static_cast<size_t>(chans)];
+            __nv_bfloat16* st = a.state + static_cast<size_t>(r) * (kTaps - 1) * chans + c;
+            r0.load(st);
+            r1.load(st + chans);
+            r2.load(st + 2 * static_cast<size_t>(chans));
             // the last three inputs of the request, or of the old state
             const int n = e - s;
-            const __nv_bfloat16 n2 = in[(e - 1) * Dp];
-            const __nv_bfloat16 n1 = n >= 2 ? in[(e - 2) * Dp] : r2;
-            const __nv_bfloat16 n0 = n >= 3 ? in[(e - 3) * Dp] : n == 2 ? r2 : r1;
-            st[0] = n0;
-            st[chans] = n1;
-            st[2 * static_cast<size_t>(chans)] = n2;
+            Chans<VEC> n0 = n == 2 ? r2 : r1, n1 = r2, n2;
+            n2.load(in + (e - 1) * Dp);
+            if (n >= 2) n1.load(in + (e - 2) * Dp);
+            if (n >= 3) n0.load(in + (e - 3) * Dp);
+            n0.store(st);
+            n1.store(st + chans);
+            n2.store(st + 2 * static_cast<size_t>(chans));
         } else if (from < to) {
-            r0 = in[(from - 3) * Dp];
-            r1 = in[(from - 2) * Dp];
-            r2 = in[(from - 1) * Dp];
+            r0.load(in + (from - 3) * Dp);
+            r1.load(in + (from - 2) * Dp);
+            r2.load(in + (from - 1) * Dp);
         }
-        for (int t = from; t < to; ++t) {
-            const __nv_bfloat16 raw = in[t * Dp];
-            float o = bias;
-            o = fmaf(w.x, bf(r0), o);
-            o = fmaf(w.y, bf(r1), o);
-            o = fmaf(w.z, bf(r2), o);
-            o = fmaf(w.w, bf(raw), o);
+        auto token = [&](const Chans<VEC>& raw, int t) {
+            float v[VEC];
+            bool sure[VEC];
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                float o = bias[i];
+                o = fmaf(w[i][0], r0.get(i), o);
+                o = fmaf(w[i][1], r1.get(i), o);
+                o = fmaf(w[i][2], r2.get(i), o);
+                o = fmaf(w[i][3], raw.get(i), o);
+                v[i] = silu_fast(o, sure[i]);
+                if (!sure[i]) v[i] = bf(silu_exact(o));
+            }
+            Chans<VEC> y;
+            if constexpr (VEC == 8)
+                y.u = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
+                                 pack_bf16(v[6], v[7]));
+            else
+                y.u = __float2bfloat16_rn(v[0]);
+            y.store(dst + static_cast<size_t>(t) * width);
             r0 = r1;
             r1 = r2;
             r2 = raw;
-            dst[static_cast<size_t>(t) * width] = __float2bfloat16_rn(o / (1.0f + expf(-o)));
+        };
+        int t = from;
+        for (; t + 4 <= to; t += 4) {
+            Chans<VEC> raw[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) raw[k].load(in + (t + k) * Dp);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) token(raw[k], t + k);
+        }
+        for (; t < to; ++t) {
+            Chans<VEC> raw;
+            raw.load(in + t * Dp);
+            token(raw, t);
         }
     }
 }
 
-__device__ __forceinline__ float block_sum(float v, float* red) {
+__device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int off = 16; off >= 1; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    return v;
+}
+
+// Sum over the `warps` warps that share a row (consecutive warps of the CTA);
+// red holds one float per warp of the CTA. Every thread of the CTA calls it
+// when warps > 1.
+__device__ __forceinline__ float row_sum(float v, int warps, float* red) {
+    v = warp_sum(v);
+    if (warps == 1) return v;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, first = warp & ~(warps - 1);
     __syncthreads();  // an earlier sum's readers are done
     if (lane == 0) red[warp] = v;
     __syncthreads();
     float s = 0.f;
-    for (int i = 0; i < static_cast<int>(blockDim.x >> 5); ++i) s += red[i];
+    for (int i = 0; i < warps; ++i) s += red[first + i];
     return s;
 }
 
-// One CTA per (row, group).
-__global__ void __launch_bounds__(kNormThreads) k_gate_norm_prompt(int din, int G, size_t Dp, const float* __restrict__ y,
-                                                                   const __nv_bfloat16* __restrict__ zx,
-                                                                   const float* __restrict__ nw, float eps,
-                                                                   __nv_bfloat16* __restrict__ out) {
+// ---------------------------------------------------------------------------
+// Gated norm, rows whose groups split into 16-byte pieces: `warps` warps per
+// (row, group), up to 16 elements of it per lane in registers (lane l of the
+// part takes elements 8 l .. 8 l + 7 and those 256 x warps on), so y and z are
+// read once. A team of warps keeps its group, so its weights stay in
+// registers, and takes every (teams / G)-th row. The sigmoid is
+// rcp(1 + 2^(-z log2 e)) from the approximate instructions, 2e-6 of it at
+// worst over |z| < 20, far inside the bf16 rounding of the result.
+// B200, 131072 rows of 4096 (8 groups; 4.29 GB): @GATE@.
+// ---------------------------------------------------------------------------
+__global__ void __launch_bounds__(kNormThreads) k_gate_norm_rows(int rows, int gs, int G, int warps, size_t Dp,
+                                                                 const float* __restrict__ y,
+                                                                 const __nv_bfloat16* __restrict__ zx,
+                                                                 const float* __restrict__ nw, float eps,
+                                                                 __nv_bfloat16* __restrict__ out) {
     __shared__ float red[kNormThreads / 32];
-    const int gs = din / G;
-    const size_t row = blockIdx.x;
+    const int per_cta = kNormThreads / 32 / warps;
+    const long long team0 = static_cast<long long>(blockIdx.x) * per_cta, team = team0 + (threadIdx.x >> 5) / warps;
+    const long long teams = static_cast<long long>(gridDim.x) * per_cta;  // a multiple of G
+    const int g = static_cast<int>(team % G);
+    const int l = threadIdx.x & (32 * warps - 1);
+    const size_t din = static_cast<size_t>(gs) * G, off = static_cast<size_t>(g) * gs;
+    int at[2];
+    bool in[2];
+    float4 w[2][2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        at[k] = 8 * (l + 32 * warps * k);
+        in[k] = at[k] < gs;
+        const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+        const float4* p = reinterpret_cast<const float4*>(nw + off + at[k]);
+        w[k][0] = in[k] ? p[0] : zero;
+        w[k][1] = in[k] ? p[1] : zero;
+    }
+    const float inv_n = 1.0f / static_cast<float>(gs);
+    const long long step = teams / G;
+    for (long long row0 = team0 / G; row0 < rows; row0 += step) {
+        // every team of the CTA goes round together (row_sum); the last rows may be missing
+        const long long row = row0 + (team / G - team0 / G);
+        const bool live = row < rows;
+        float v[2][8];
+        float ss = 0.f;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            float4 a0 = make_float4(0.f, 0.f, 0.f, 0.f), a1 = a0;
+            uint4 z = make_uint4(0, 0, 0, 0);
+            if (live && in[k]) {
+                const float4* py = reinterpret_cast<const float4*>(y + row * din + off + at[k]);
+                a0 = py[0];
+                a1 = py[1];
+                z = *reinterpret_cast<const uint4*>(zx + row * Dp + off + at[k]);
+            }
+            const float ya[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
+            const uint32_t zw[4] = {z.x, z.y, z.z, z.w};
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float zf = i & 1 ? bf_hi(zw[i / 2]) : bf_lo(zw[i / 2]);
+                v[k][i] = ya[i] * (zf * rcp_approx(1.0f + ex2_approx(zf * -1.4426950408889634f)));
+                ss = fmaf(v[k][i], v[k][i], ss);
+            }
+        }
+        const float inv = rsqrtf(row_sum(ss, warps, red) * inv_n + eps);
+        if (!live) continue;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            if (!in[k]) continue;
+            const float ww[8] = {w[k][0].x, w[k][0].y, w[k][0].z, w[k][0].w, w[k][1].x, w[k][1].y, w[k][1].z, w[k][1].w};
+            uint32_t o[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                o[i] = pack_bf16(v[k][2 * i] * inv * ww[2 * i], v[k][2 * i + 1] * inv * ww[2 * i + 1]);
+            *reinterpret_cast<uint4*>(out + row * din + off + at[k]) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+    }
+}
+
+// Any other group size or row stride: one CTA per (row, group), element by element.
+__global__ void __launch_bounds__(kNormThreads) k_gate_norm_any(int gs, int G, size_t Dp, const float* __restrict__ y,
+                                                                const __nv_bfloat16* __restrict__ zx,
+                                                                const float* __restrict__ nw, float eps,
+                                                                __nv_bfloat16* __restrict__ out) {
+    __shared__ float red[kNormThreads / 32];
+    const size_t row = blockIdx.x, din = static_cast<size_t>(gs) * G;
     const size_t off = static_cast<size_t>(blockIdx.y) * gs;
     const float* yr = y + row * din + off;
     const __nv_bfloat16* zr = zx + row * Dp + off;
@@ -168,13 +351,13 @@ __global__ void __launch_bounds__(kNormThreads) k_gate_norm_prompt(int din, int 
         const float g = gated(i);
         ss = fmaf(g, g, ss);
     }
-    const float inv = rsqrtf(block_sum(ss, red) / static_cast<float>(gs) + eps);
+    const float inv = rsqrtf(row_sum(ss, kNormThreads / 32, red) / static_cast<float>(gs) + eps);
     for (int i = threadIdx.x; i < gs; i += kNormThreads)
         out[row * din + off + i] = __float2bfloat16_rn(gated(i) * inv * nw[off + i]);
 }
 
 struct AddNormArgs {
-    int dim;
+    int rows, dim;
     const void* u;
     const __nv_bfloat16* v;
     const float* post_w;
@@ -186,30 +369,136 @@ struct AddNormArgs {
     __nv_bfloat16* out;
 };
 
+// Eight stream values from and to memory, and rounded as memory keeps them.
+__device__ __forceinline__ void load8(const float* p, float (&f)[8]) {
+    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&f)[8]) {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[2 * i] = bf_lo(w[i]), f[2 * i + 1] = bf_hi(w[i]);
+}
+__device__ __forceinline__ void store8(float* p, float (&f)[8], bool write) {
+    if (!write) return;
+    reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, float (&f)[8], bool write) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        w[i] = pack_bf16(f[2 * i], f[2 * i + 1]);
+        f[2 * i] = bf_lo(w[i]), f[2 * i + 1] = bf_hi(w[i]);
+    }
+    if (write) *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
 __device__ __forceinline__ float to_f(float v) { return v; }
 __device__ __forceinline__ float to_f(__nv_bfloat16 v) { return bf(v); }
 __device__ __forceinline__ void put(float* p, float v) { *p = v; }
 __device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
-// One CTA per row.
+// ---------------------------------------------------------------------------
+// Add and norms, dim a multiple of 8: `warps` warps per row, up to 32 elements
+// of it per lane in registers (four pieces of 8, 256 x warps apart), so u and
+// v are read once and both sums of squares are taken from registers.
+// B200, 131072 rows of 2048, bf16 stream, every option (2.15 GB): @ADD@.
+// ---------------------------------------------------------------------------
 template <typename TU>
-__global__ void __launch_bounds__(kNormThreads) k_add_norm(const AddNormArgs a) {
+__global__ void __launch_bounds__(512) k_add_norm_rows(const AddNormArgs a, const int warps) {
+    __shared__ float red[16];
+    const int l = threadIdx.x & (32 * warps - 1);
+    const long long row = static_cast<long long>(blockIdx.x) * (blockDim.x / 32 / warps) + (threadIdx.x >> 5) / warps;
+    const bool live = row < a.rows;
+    const float inv_n = 1.0f / static_cast<float>(a.dim);
+    const size_t r0 = static_cast<size_t>(live ? row : 0) * a.dim;
+    float u[4][8], v[4][8];
+    float ss = 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int at = 8 * (l + 32 * warps * k);
+        const bool in = live && at < a.dim;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) u[k][i] = v[k][i] = 0.f;
+        if (in) load8(static_cast<const TU*>(a.u) + r0 + at, u[k]);
+        if (in && a.v) load8(a.v + r0 + at, v[k]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ss = fmaf(v[k][i], v[k][i], ss);
+    }
+    if (a.v) {
+        const float inv = a.post_w ? rsqrtf(row_sum(ss, warps, red) * inv_n + a.eps) : 1.0f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int at = 8 * (l + 32 * warps * k);
+            if (at >= a.dim) continue;
+            float f[8];
+            if (a.post_w) {
+                load8(a.post_w + at, f);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[k][i] = v[k][i] * inv * f[i];
+            }
+            if (a.gate) {
+                load8(a.gate + at, f);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[k][i] *= f[i];
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) u[k][i] = fmaf(a.scale, v[k][i], u[k][i]);
+        }
+    }
+    ss = 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int at = 8 * (l + 32 * warps * k);
+        const bool in = live && at < a.dim;
+        store8(static_cast<TU*>(a.u_out) + r0 + (in ? at : 0), u[k], in && a.u_out);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ss = fmaf(u[k][i], u[k][i], ss);
+    }
+    if (!a.out) return;
+    const float pre = rsqrtf(row_sum(ss, warps, red) * inv_n + a.eps);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int at = 8 * (l + 32 * warps * k);
+        if (!live || at >= a.dim) continue;
+        float f[8];
+        load8(a.pre_w + at, f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = u[k][i] * pre * f[i];
+        store8(a.out + r0 + at, f, true);
+    }
+}
+
+// Any other width: one CTA per row, element by element, 16 elements per
+// thread in registers and the rest of a wide row read again.
+constexpr int kAddKeep = 16;
+template <typename TU>
+__global__ void __launch_bounds__(kNormThreads) k_add_norm_any(const AddNormArgs a) {
     __shared__ float red[kNormThreads / 32];
-    const size_t row = blockIdx.x;
+    constexpr int kW = kNormThreads / 32;
+    const size_t r0 = static_cast<size_t>(blockIdx.x) * a.dim;
     const int dim = a.dim;
-    const TU* u = static_cast<const TU*>(a.u) + row * dim;
-    TU* uo = a.u_out ? static_cast<TU*>(a.u_out) + row * dim : nullptr;
-    const __nv_bfloat16* v = a.v ? a.v + row * dim : nullptr;
+    const TU* u = static_cast<const TU*>(a.u) + r0;
+    TU* uo = a.u_out ? static_cast<TU*>(a.u_out) + r0 : nullptr;
+    const __nv_bfloat16* v = a.v ? a.v + r0 : nullptr;
+    float ku[kAddKeep], kv[kAddKeep];
+#pragma unroll
+    for (int k = 0; k < kAddKeep; ++k) {
+        const int i = threadIdx.x + k * kNormThreads;
+        ku[k] = i < dim ? to_f(u[i]) : 0.f;
+        kv[k] = v && i < dim ? bf(v[i]) : 0.f;
+    }
     float inv = 1.f;
     if (v && a.post_w) {
         float ss = 0.f;
-        for (int i = threadIdx.x; i < dim; i += kNormThreads) ss = fmaf(bf(v[i]), bf(v[i]), ss);
-        inv = rsqrtf(block_sum(ss, red) / static_cast<float>(dim) + a.eps);
+#pragma unroll
+        for (int k = 0; k < kAddKeep; ++k) ss = fmaf(kv[k], kv[k], ss);
+        for (int i = threadIdx.x + kAddKeep * kNormThreads; i < dim; i += kNormThreads) ss = fmaf(bf(v[i]), bf(v[i]), ss);
+        inv = rsqrtf(row_sum(ss, kW, red) / static_cast<float>(dim) + a.eps);
     }
-    auto stream = [&](int i) {  // u' as it is kept
-        float t = to_f(u[i]);
+    auto stream = [&](int i, float t, float f) {  // u' as it is kept
         if (v) {
-            float f = bf(v[i]);
             if (a.post_w) f = f * inv * a.post_w[i];
             if (a.gate) f *= a.gate[i];
             t = fmaf(a.scale, f, t);
@@ -218,22 +507,45 @@ __global__ void __launch_bounds__(kNormThreads) k_add_norm(const AddNormArgs a) 
         put(&k, t);
         return k;
     };
-    if (!a.out) {
-        if (uo)
-            for (int i = threadIdx.x; i < dim; i += kNormThreads) uo[i] = stream(i);
-        return;
-    }
     float ss = 0.f;
-    for (int i = threadIdx.x; i < dim; i += kNormThreads) {
-        const float t = to_f(stream(i));
-        ss = fmaf(t, t, ss);
+#pragma unroll
+    for (int k = 0; k < kAddKeep; ++k) {
+        const int i = threadIdx.x + k * kNormThreads;
+        if (i < dim) {
+            const TU t = stream(i, ku[k], kv[k]);
+            if (uo) uo[i] = t;
+            ku[k] = to_f(t);
+        }
+        ss = fmaf(ku[k], ku[k], ss);
     }
-    const float pre = rsqrtf(block_sum(ss, red) / static_cast<float>(dim) + a.eps);
-    for (int i = threadIdx.x; i < dim; i += kNormThreads) {
-        const TU k = stream(i);
-        if (uo) uo[i] = k;
-        a.out[row * dim + i] = __float2bfloat16_rn(to_f(k) * pre * a.pre_w[i]);
+    for (int i = threadIdx.x + kAddKeep * kNormThreads; i < dim; i += kNormThreads) {
+        const TU t = stream(i, to_f(u[i]), v ? bf(v[i]) : 0.f);
+        if (a.out) ss = fmaf(to_f(t), to_f(t), ss);
+        if (uo && !a.out) uo[i] = t;
     }
+    if (!a.out) return;
+    const float pre = rsqrtf(row_sum(ss, kW, red) / static_cast<float>(dim) + a.eps);
+#pragma unroll
+    for (int k = 0; k < kAddKeep; ++k) {
+        const int i = threadIdx.x + k * kNormThreads;
+        if (i < dim) a.out[r0 + i] = __float2bfloat16_rn(ku[k] * pre * a.pre_w[i]);
+    }
+    for (int i = threadIdx.x + kAddKeep * kNormThreads; i < dim; i += kNormThreads) {
+        const TU t = stream(i, to_f(u[i]), v ? bf(v[i]) : 0.f);
+        if (uo) uo[i] = t;
+        a.out[r0 + i] = __float2bfloat16_rn(to_f(t) * pre * a.pre_w[i]);
+    }
+}
+
+// Streaming multiprocessors of the current device.
+int sm_count() {
+    static std::atomic<int> cache[64];
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return 148;
+    if (dev < 64 && (n = cache[dev].load(std::memory_order_relaxed)) > 0) return n;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) return 148;
+    if (dev < 64) cache[dev].store(n, std::memory_order_relaxed);
+    return n;
 }
 
 rssm_status_t prompt_shape_ok(const rssm_desc_t* d) {
@@ -285,11 +597,21 @@ rssm_status_t rssm_stage_conv_prompt(const rssm_desc_t* d, int32_t total, const 
     a.C = static_cast<__nv_bfloat16*>(C);
     a.dt = dt;
     a.err = err;
-    const int lanes = a.din + 2 * a.gn + a.H;
-    const dim3 grid(static_cast<unsigned>((total - 1) / kConvTok + 1),
-                    static_cast<unsigned>((lanes + kConvThreads - 1) / kConvThreads));
-    if (grid.y > 65535) return RSSM_ERR_SHAPE;
-    k_conv_prompt<<<grid, kConvThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
+    // 16-byte accesses when every row and each of x, B, C starts on 16 bytes
+    const int chans = a.din + 2 * a.gn;
+    const bool vec = a.din % 8 == 0 && a.gn % 8 == 0 && a.H % 8 == 0;
+    const int per_cta = (vec ? 8 : 1) * kConvThreads;
+    const int ny = (chans + per_cta - 1) / per_cta + 1;  // and the dt heads
+    if (ny > 65535) return RSSM_ERR_SHAPE;
+    // Tokens per CTA: 32 (three rows before them are read again), fewer while
+    // that leaves SMs without work
+    a.tok = 32;
+    while (a.tok > 4 && static_cast<long long>((total - 1) / a.tok + 1) * ny < 4ll * sm_count()) a.tok /= 2;
+    const dim3 grid(static_cast<unsigned>((total - 1) / a.tok + 1), static_cast<unsigned>(ny));
+    if (vec)
+        k_conv_prompt<8><<<grid, kConvThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
+    else
+        k_conv_prompt<1><<<grid, kConvThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
     return launched();
 }
 
@@ -302,10 +624,29 @@ rssm_status_t rssm_stage_gate_norm_prompt(const rssm_desc_t* d, int32_t rows, co
     if (!y || !zxbcdt || !out || !aligned16({y, zxbcdt, norm_w, out})) return RSSM_ERR_INVALID_ARG;
     const int din = d->nheads * d->head_dim, G = d->ngroups;
     const size_t Dp = 2 * static_cast<size_t>(din) + 2 * static_cast<size_t>(G) * d->d_state + d->nheads;
+    const int gs = din / G;
+    const __nv_bfloat16* zx = static_cast<const __nv_bfloat16*>(zxbcdt);
+    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(out);
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    // 16-byte pieces, and a group within 16 elements of each thread of a CTA
+    if (gs % 8 == 0 && Dp % 8 == 0 && gs <= 16 * kNormThreads) {
+        int warps = 1;
+        while (512 * warps < gs) warps *= 2;
+        const int per_cta = kNormThreads / 32 / warps;  // teams
+        // teams a multiple of G (a team keeps its group): whole rounds of G CTAs
+        // or, when a CTA has a multiple of G teams, any number of CTAs; as many
+        // as the GPU holds (8 CTAs per SM), no more than there are rows
+        const long long unit = per_cta % G == 0 ? 1 : G, rows_per_unit = unit * per_cta / G;
+        const long long want = (rows + rows_per_unit - 1) / rows_per_unit;
+        const long long hold = (8ll * sm_count() + unit - 1) / unit;
+        const long long units = want < hold ? want : hold;
+        k_gate_norm_rows<<<static_cast<unsigned>(units * unit), kNormThreads, 0, st>>>(rows, gs, G, warps, Dp, y, zx,
+                                                                                       norm_w, eps, o);
+        return launched();
+    }
     if (G > 65535) return RSSM_ERR_SHAPE;
     const dim3 grid(static_cast<unsigned>(rows), static_cast<unsigned>(G));
-    k_gate_norm_prompt<<<grid, kNormThreads, 0, static_cast<cudaStream_t>(stream)>>>(
-        din, G, Dp, y, static_cast<const __nv_bfloat16*>(zxbcdt), norm_w, eps, static_cast<__nv_bfloat16*>(out));
+    k_gate_norm_any<<<grid, kNormThreads, 0, st>>>(gs, G, Dp, y, zx, norm_w, eps, o);
     return launched();
 }
 
@@ -320,6 +661,7 @@ rssm_status_t rssm_stage_add_norm(int32_t rows, int32_t dim, int32_t u_dtype, co
     if (!u || (v && !u_out)) return RSSM_ERR_INVALID_ARG;
     if (!aligned16({u, v, post_w, gate, pre_w, u_out, out})) return RSSM_ERR_INVALID_ARG;
     AddNormArgs a;
+    a.rows = rows;
     a.dim = dim;
     a.u = u;
     a.v = static_cast<const __nv_bfloat16*>(v);
@@ -330,11 +672,21 @@ rssm_status_t rssm_stage_add_norm(int32_t rows, int32_t dim, int32_t u_dtype, co
     a.eps = eps;
     a.u_out = u_out;
     a.out = static_cast<__nv_bfloat16*>(out);
-    const unsigned grid = static_cast<unsigned>(rows);
-    if (u_dtype == RSSM_F32)
-        k_add_norm<float><<<grid, kNormThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
-    else
-        k_add_norm<__nv_bfloat16><<<grid, kNormThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (dim % 8 == 0) {
+        int warps = 1;  // per row, 1024 elements each
+        while (1024 * warps < dim) warps *= 2;
+        const int threads = warps > 8 ? 32 * warps : 256, per_cta = threads / 32 / warps;
+        const unsigned grid = static_cast<unsigned>((rows - 1) / per_cta + 1);
+        if (u_dtype == RSSM_F32)
+            k_add_norm_rows<float><<<grid, threads, 0, st>>>(a, warps);
+        else
+            k_add_norm_rows<__nv_bfloat16><<<grid, threads, 0, st>>>(a, warps);
+    } else if (u_dtype == RSSM_F32) {
+        k_add_norm_any<float><<<static_cast<unsigned>(rows), kNormThreads, 0, st>>>(a);
+    } else {
+        k_add_norm_any<__nv_bfloat16><<<static_cast<unsigned>(rows), kNormThreads, 0, st>>>(a);
+    }
     return launched();
 }
 
