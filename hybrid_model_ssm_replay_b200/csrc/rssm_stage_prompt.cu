@@ -58,37 +58,66 @@ struct ConvPromptArgs {
 };
 
 // silu as rssm_stage_conv forms it, in bf16.
-__device__ __noinline__ __nv_bfloat16 silu_exact(float o) { return __float2bfloat16_rn(o / (1.0f + expf(-o))); }
-
-// The same bits for less: o rcp(1 + 2^(-o log2 e)) from the approximate
-// instructions is, for |o| < 32, within 23 fp32 spacings of the quotient (19
-// from the argument -o log2 e, up to 46 in size, 2 of ex2, 1 of rcp, 1 of the
-// add and the product) and the library form within 3, so both round to the
-// same bf16 unless the value lies within 32 spacings of the middle between
-// two bf16 (one value in a thousand), which take the library form.
-__device__ __forceinline__ float silu_fast(float o, bool& sure) {
-    const float v = o * rcp_approx(1.0f + ex2_approx(o * -1.4426950408889634f));
-    const uint32_t off = (__float_as_uint(v) - (0x8000u - 32u)) & 0xFFFFu;
-    sure = off > 64u && fabsf(o) < 32.0f && fabsf(v) > 1e-30f;
-    return v;
+__device__ __noinline__ uint16_t silu_exact(float o) {
+    return __bfloat16_as_ushort(__float2bfloat16_rn(o / (1.0f + expf(-o))));
 }
 
-template <int VEC> struct Chans;  // VEC consecutive channels as they are kept
-template <> struct Chans<8> {
-    uint4 u;
-    __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = *reinterpret_cast<const uint4*>(p); }
-    __device__ __forceinline__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = u; }
-    __device__ __forceinline__ float get(int i) const {
-        const uint32_t w = i < 2 ? u.x : i < 4 ? u.y : i < 6 ? u.z : u.w;
-        return i & 1 ? bf_hi(w) : bf_lo(w);
-    }
-};
-template <> struct Chans<1> {
-    __nv_bfloat16 u;
-    __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = *p; }
-    __device__ __forceinline__ void store(__nv_bfloat16* p) const { *p = u; }
-    __device__ __forceinline__ float get(int) const { return bf(u); }
-};
+// Two fp32 lanes in one instruction, each as the scalar one rounds.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\t"
+        "mov.b64 ra, {%2, %3};\n\t"
+        "mov.b64 rb, {%4, %5};\n\t"
+        "mov.b64 rc, {%6, %7};\n\t"
+        "fma.rn.f32x2 rd, ra, rb, rc;\n\t"
+        "mov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
+        "mov.b64 ra, {%2, %3};\n\t"
+        "mov.b64 rb, {%4, %5};\n\t"
+        "mul.rn.f32x2 rd, ra, rb;\n\t"
+        "mov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
+        "mov.b64 ra, {%2, %3};\n\t"
+        "mov.b64 rb, {%4, %5};\n\t"
+        "add.rn.f32x2 rd, ra, rb;\n\t"
+        "mov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
+// silu of two channels as a pair of bf16, the bits of silu_exact for less:
+// o / (1 + 2^(-o log2 e)) with the approximate exponential and one
+// approximate reciprocal of both denominators' product, 1/a = b rcp(a b).
+// For |o| < 32 that is within 26 fp32 spacings of the quotient (19 from the
+// argument -o log2 e, up to 46 in size, 2 of ex2, 1 of rcp, 4 of the add and
+// the products) and the library form within 3, so both round to the same
+// bf16 unless the value lies within 32 spacings of the middle between two
+// bf16: one value in a thousand, which takes the library form.
+__device__ __forceinline__ uint32_t silu2(float2 o) {
+    const float2 t = mul2(o, make_float2(-1.4426950408889634f, -1.4426950408889634f));
+    const float2 d = add2(make_float2(ex2_approx(t.x), ex2_approx(t.y)), make_float2(1.0f, 1.0f));
+    const float r = rcp_approx(d.x * d.y);
+    const float2 v = mul2(o, mul2(make_float2(d.y, d.x), make_float2(r, r)));
+    uint32_t w = pack_bf16(v.x, v.y);
+    const uint32_t o0 = (__float_as_uint(v.x) - (0x8000u - 32u)) & 0xFFFFu;
+    const uint32_t o1 = (__float_as_uint(v.y) - (0x8000u - 32u)) & 0xFFFFu;
+    if (!(min(o0, o1) > 64u && fmaxf(fabsf(o.x), fabsf(o.y)) < 32.0f))
+        w = silu_exact(o.x) | (static_cast<uint32_t>(silu_exact(o.y)) << 16);
+    return w;
+}
 
 // The first request that ends past token t: each lane tries a part of the range.
 __device__ __forceinline__ int first_request(const int32_t* cu, int batch, int t) {
@@ -119,8 +148,30 @@ __device__ __forceinline__ int first_request(const int32_t* cu, int batch, int t
 // flight per thread. B200, 256 prompts of 512 tokens, 6144 channels (3.29 GB):
 // @CONV@.
 // ---------------------------------------------------------------------------
+// What a thread of k_conv_prompt has of its channels: VEC as one load brings
+// them, as floats, and the products.
+template <int VEC> struct Chans;
+template <> struct Chans<8> {
+    using Raw = uint4;
+    float2 f[4];
+    __device__ __forceinline__ void set(const Raw& u) {
+        f[0] = make_float2(bf_lo(u.x), bf_hi(u.x));
+        f[1] = make_float2(bf_lo(u.y), bf_hi(u.y));
+        f[2] = make_float2(bf_lo(u.z), bf_hi(u.z));
+        f[3] = make_float2(bf_lo(u.w), bf_hi(u.w));
+    }
+};
+template <> struct Chans<1> {
+    using Raw = uint16_t;
+    float2 f[1];
+    __device__ __forceinline__ void set(const Raw& u) { f[0] = make_float2(bf_lo(u), 0.f); }
+};
+
 template <int VEC>
-__global__ void __launch_bounds__(kConvThreads) k_conv_prompt(const ConvPromptArgs a) {
+__global__ void __launch_bounds__(kConvThreads, 2) k_conv_prompt(const ConvPromptArgs a) {
+    using Raw = typename Chans<VEC>::Raw;
+    constexpr int kPairs = (VEC + 1) / 2;
+    constexpr int kAhead = 4;  // rows fetched before the ones at work
     const int chans = a.din + 2 * a.gn;
     const size_t Dp = static_cast<size_t>(a.din) + chans + a.H;
     const int t0 = blockIdx.x * a.tok, t1 = min(a.total - t0, a.tok) + t0;
@@ -145,15 +196,16 @@ __global__ void __launch_bounds__(kConvThreads) k_conv_prompt(const ConvPromptAr
     }
     const int c = VEC * (blockIdx.y * kConvThreads + threadIdx.x);
     if (c >= chans) return;
-    float w[VEC][kTaps], bias[VEC];
+    float2 w[kTaps][kPairs], bias[kPairs];
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-        const float4 v = reinterpret_cast<const float4*>(a.w)[c + i];
-        w[i][0] = v.x;
-        w[i][1] = v.y;
-        w[i][2] = v.z;
-        w[i][3] = v.w;
-        bias[i] = a.bias[c + i];
+    for (int i = 0; i < kPairs; ++i) {
+        const int c1 = c + 2 * i + (VEC > 1);  // (VEC 1: the pair's second half is not used)
+        const float4 v0 = reinterpret_cast<const float4*>(a.w)[c + 2 * i], v1 = reinterpret_cast<const float4*>(a.w)[c1];
+        w[0][i] = make_float2(v0.x, v1.x);
+        w[1][i] = make_float2(v0.y, v1.y);
+        w[2][i] = make_float2(v0.z, v1.z);
+        w[3][i] = make_float2(v0.w, v1.w);
+        bias[i] = make_float2(a.bias[c + 2 * i], a.bias[c1]);
     }
     const __nv_bfloat16* in = a.zx + a.din + c;
     __nv_bfloat16* dst;
@@ -168,6 +220,7 @@ __global__ void __launch_bounds__(kConvThreads) k_conv_prompt(const ConvPromptAr
         dst = a.C + (c - a.din - a.gn);
         width = a.gn;
     }
+    auto row = [&](int t) { return *reinterpret_cast<const Raw*>(in + static_cast<size_t>(t) * Dp); };
     for (int r = request0; r < a.batch; ++r) {
         const int s = a.cu[r], e = a.cu[r + 1];
         if (s >= t1) break;
@@ -175,62 +228,55 @@ __global__ void __launch_bounds__(kConvThreads) k_conv_prompt(const ConvPromptAr
         const bool first = s >= t0;
         const int from = first ? s : max(t0, s + kTaps - 1);
         const int to = first ? max(min(e, t1), min(e, s + kTaps - 1)) : min(e, t1);
-        Chans<VEC> r0, r1, r2;
+        Chans<VEC> r0, r1, r2;  // the three inputs before the token
         if (first) {
             __nv_bfloat16* st = a.state + static_cast<size_t>(r) * (kTaps - 1) * chans + c;
-            r0.load(st);
-            r1.load(st + chans);
-            r2.load(st + 2 * static_cast<size_t>(chans));
+            Raw* s0 = reinterpret_cast<Raw*>(st);
+            Raw* s1 = reinterpret_cast<Raw*>(st + chans);
+            Raw* s2 = reinterpret_cast<Raw*>(st + 2 * static_cast<size_t>(chans));
+            const Raw o0 = *s0, o1 = *s1, o2 = *s2;
+            r0.set(o0);
+            r1.set(o1);
+            r2.set(o2);
             // the last three inputs of the request, or of the old state
             const int n = e - s;
-            Chans<VEC> n0 = n == 2 ? r2 : r1, n1 = r2, n2;
-            n2.load(in + (e - 1) * Dp);
-            if (n >= 2) n1.load(in + (e - 2) * Dp);
-            if (n >= 3) n0.load(in + (e - 3) * Dp);
-            n0.store(st);
-            n1.store(st + chans);
-            n2.store(st + 2 * static_cast<size_t>(chans));
+            *s0 = n >= 3 ? row(e - 3) : n == 2 ? o2 : o1;
+            *s1 = n >= 2 ? row(e - 2) : o2;
+            *s2 = row(e - 1);
         } else if (from < to) {
-            r0.load(in + (from - 3) * Dp);
-            r1.load(in + (from - 2) * Dp);
-            r2.load(in + (from - 1) * Dp);
+            r0.set(row(from - 3));
+            r1.set(row(from - 2));
+            r2.set(row(from - 1));
         }
-        auto token = [&](const Chans<VEC>& raw, int t) {
-            float v[VEC];
-            bool sure[VEC];
+        Raw next[kAhead];
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                float o = bias[i];
-                o = fmaf(w[i][0], r0.get(i), o);
-                o = fmaf(w[i][1], r1.get(i), o);
-                o = fmaf(w[i][2], r2.get(i), o);
-                o = fmaf(w[i][3], raw.get(i), o);
-                v[i] = silu_fast(o, sure[i]);
-                if (!sure[i]) v[i] = bf(silu_exact(o));
+        for (int k = 0; k < kAhead; ++k)
+            if (from + k < to) next[k] = row(from + k);
+        for (int t = from; t < to; t += kAhead) {
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                if (t + k >= to) break;
+                Chans<VEC> cur;
+                cur.set(next[k]);
+                if (t + kAhead + k < to) next[k] = row(t + kAhead + k);
+                uint32_t y[kPairs];
+#pragma unroll
+                for (int i = 0; i < kPairs; ++i) {
+                    float2 o = fma2(w[0][i], r0.f[i], bias[i]);
+                    o = fma2(w[1][i], r1.f[i], o);
+                    o = fma2(w[2][i], r2.f[i], o);
+                    o = fma2(w[3][i], cur.f[i], o);
+                    y[i] = silu2(o);
+                }
+                __nv_bfloat16* to_y = dst + static_cast<size_t>(t + k) * width;
+                if constexpr (VEC == 8)
+                    *reinterpret_cast<uint4*>(to_y) = make_uint4(y[0], y[1], y[2], y[3]);
+                else
+                    *reinterpret_cast<uint16_t*>(to_y) = static_cast<uint16_t>(y[0]);
+                r0 = r1;
+                r1 = r2;
+                r2 = cur;
             }
-            Chans<VEC> y;
-            if constexpr (VEC == 8)
-                y.u = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
-                                 pack_bf16(v[6], v[7]));
-            else
-                y.u = __float2bfloat16_rn(v[0]);
-            y.store(dst + static_cast<size_t>(t) * width);
-            r0 = r1;
-            r1 = r2;
-            r2 = raw;
-        };
-        int t = from;
-        for (; t + 4 <= to; t += 4) {
-            Chans<VEC> raw[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) raw[k].load(in + (t + k) * Dp);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) token(raw[k], t + k);
-        }
-        for (; t < to; ++t) {
-            Chans<VEC> raw;
-            raw.load(in + t * Dp);
-            token(raw, t);
         }
     }
 }
@@ -369,31 +415,41 @@ struct AddNormArgs {
     __nv_bfloat16* out;
 };
 
-// Eight stream values from and to memory, and rounded as memory keeps them.
-__device__ __forceinline__ void load8(const float* p, float (&f)[8]) {
-    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
-}
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&f)[8]) {
-    const uint4 u = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+// Eight consecutive values as they are kept in memory.
+template <typename T> struct Eight;
+template <> struct Eight<__nv_bfloat16> {
+    uint4 u;
+    __device__ __forceinline__ void zero() { u = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = *reinterpret_cast<const uint4*>(p); }
+    __device__ __forceinline__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = u; }
+    __device__ __forceinline__ void get(float (&f)[8]) const {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) f[2 * i] = bf_lo(w[i]), f[2 * i + 1] = bf_hi(w[i]);
-}
-__device__ __forceinline__ void store8(float* p, float (&f)[8], bool write) {
-    if (!write) return;
-    reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
-}
-__device__ __forceinline__ void store8(__nv_bfloat16* p, float (&f)[8], bool write) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        w[i] = pack_bf16(f[2 * i], f[2 * i + 1]);
-        f[2 * i] = bf_lo(w[i]), f[2 * i + 1] = bf_hi(w[i]);
+        for (int i = 0; i < 4; ++i) f[2 * i] = bf_lo(w[i]), f[2 * i + 1] = bf_hi(w[i]);
     }
-    if (write) *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-}
+    __device__ __forceinline__ void set(const float (&f)[8]) {
+        u = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+    }
+};
+template <> struct Eight<float> {
+    float4 a, b;
+    __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+    __device__ __forceinline__ void load(const float* p) {
+        a = reinterpret_cast<const float4*>(p)[0];
+        b = reinterpret_cast<const float4*>(p)[1];
+    }
+    __device__ __forceinline__ void store(float* p) const {
+        reinterpret_cast<float4*>(p)[0] = a;
+        reinterpret_cast<float4*>(p)[1] = b;
+    }
+    __device__ __forceinline__ void get(float (&f)[8]) const {
+        f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+    }
+    __device__ __forceinline__ void set(const float (&f)[8]) {
+        a = make_float4(f[0], f[1], f[2], f[3]);
+        b = make_float4(f[4], f[5], f[6], f[7]);
+    }
+};
 __device__ __forceinline__ float to_f(float v) { return v; }
 __device__ __forceinline__ float to_f(__nv_bfloat16 v) { return bf(v); }
 __device__ __forceinline__ void put(float* p, float v) { *p = v; }
@@ -413,60 +469,75 @@ __global__ void __launch_bounds__(512) k_add_norm_rows(const AddNormArgs a, cons
     const bool live = row < a.rows;
     const float inv_n = 1.0f / static_cast<float>(a.dim);
     const size_t r0 = static_cast<size_t>(live ? row : 0) * a.dim;
-    float u[4][8], v[4][8];
-    float ss = 0.f;
+    auto at = [&](int k) { return 8 * (l + 32 * warps * k); };
+    Eight<TU> u[4];
+    Eight<__nv_bfloat16> v[4];
+    float f[8], g[8], ss = 0.f;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-        const int at = 8 * (l + 32 * warps * k);
-        const bool in = live && at < a.dim;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) u[k][i] = v[k][i] = 0.f;
-        if (in) load8(static_cast<const TU*>(a.u) + r0 + at, u[k]);
-        if (in && a.v) load8(a.v + r0 + at, v[k]);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(v[k][i], v[k][i], ss);
-    }
-    if (a.v) {
-        const float inv = a.post_w ? rsqrtf(row_sum(ss, warps, red) * inv_n + a.eps) : 1.0f;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int at = 8 * (l + 32 * warps * k);
-            if (at >= a.dim) continue;
-            float f[8];
-            if (a.post_w) {
-                load8(a.post_w + at, f);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[k][i] = v[k][i] * inv * f[i];
-            }
-            if (a.gate) {
-                load8(a.gate + at, f);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[k][i] *= f[i];
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) u[k][i] = fmaf(a.scale, v[k][i], u[k][i]);
+        u[k].zero();
+        v[k].zero();
+        if (live && at(k) < a.dim) {
+            u[k].load(static_cast<const TU*>(a.u) + r0 + at(k));
+            if (a.v) v[k].load(a.v + r0 + at(k));
         }
     }
-    ss = 0.f;
+    if (a.v) {
+        float inv = 1.0f;
+        if (a.post_w) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                v[k].get(f);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) ss = fmaf(f[i], f[i], ss);
+            }
+            inv = rsqrtf(row_sum(ss, warps, red) * inv_n + a.eps);
+            ss = 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (at(k) >= a.dim) continue;
+            Eight<float> c;
+            v[k].get(f);
+            if (a.post_w) {
+                c.load(a.post_w + at(k));
+                c.get(g);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) f[i] = f[i] * inv * g[i];
+            }
+            if (a.gate) {
+                c.load(a.gate + at(k));
+                c.get(g);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) f[i] *= g[i];
+            }
+            u[k].get(g);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) g[i] = fmaf(a.scale, f[i], g[i]);
+            u[k].set(g);
+        }
+    }
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-        const int at = 8 * (l + 32 * warps * k);
-        const bool in = live && at < a.dim;
-        store8(static_cast<TU*>(a.u_out) + r0 + (in ? at : 0), u[k], in && a.u_out);
+        if (a.u_out && live && at(k) < a.dim) u[k].store(static_cast<TU*>(a.u_out) + r0 + at(k));
+        u[k].get(f);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(u[k][i], u[k][i], ss);
+        for (int i = 0; i < 8; ++i) ss = fmaf(f[i], f[i], ss);
     }
     if (!a.out) return;
     const float pre = rsqrtf(row_sum(ss, warps, red) * inv_n + a.eps);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-        const int at = 8 * (l + 32 * warps * k);
-        if (!live || at >= a.dim) continue;
-        float f[8];
-        load8(a.pre_w + at, f);
+        if (!live || at(k) >= a.dim) continue;
+        Eight<float> c;
+        c.load(a.pre_w + at(k));
+        c.get(g);
+        u[k].get(f);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = u[k][i] * pre * f[i];
-        store8(a.out + r0 + at, f, true);
+        for (int i = 0; i < 8; ++i) f[i] = f[i] * pre * g[i];
+        Eight<__nv_bfloat16> o;
+        o.set(f);
+        o.store(a.out + r0 + at(k));
     }
 }
 

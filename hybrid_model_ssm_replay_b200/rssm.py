@@ -115,17 +115,29 @@ def _ptr(t, dtype=None, name="tensor"):
     return ct.c_void_p(t.data_ptr())
 
 
-def _arg(t, dtype, shape, name):
-    """_ptr of a tensor of this shape on the current device, 16-byte aligned
-    (int32 tensors: the prompts' bounds and the error word, 4-byte)."""
-    p = _ptr(t, dtype, name)
-    if p is None:
-        return None
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.device.index != torch.cuda.current_device():
+def _device(t, name):
+    """The index of the CUDA device a tensor is on, which must be the current one."""
+    dev = t.get_device() if isinstance(t, torch.Tensor) else -1
+    if dev < 0:
+        _ptr(t, None, name)  # says what is wrong
+    if dev != torch.cuda.current_device():
         raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
-    if t.data_ptr() % (4 if t.dtype == torch.int32 else 16):
+    return dev
+
+
+def _arg(t, dtype, shape, name, dev):
+    """The address of a tensor of this type and shape on device `dev` (the
+    current one), 16-byte aligned (int32 tensors, the prompts' bounds and the
+    error word: 4-byte); None for None."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype != dtype or not t.is_contiguous():
+        _ptr(t, dtype, name)  # says what is wrong
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    p = t.data_ptr()
+    if p & (3 if dtype is torch.int32 else 15):
         raise ValueError(f"{name} is not 16-byte aligned")
     return p
 
@@ -289,13 +301,13 @@ def rssm_prefill_scan(state, cu_seqlens, max_seqlen, x, B, C, dt, A, D, y, works
     tensor of rssm_prefill_scan_workspace_bytes(desc, total, max_seqlen), or
     None to allocate it for the call."""
     d = state.desc
-    in_dt, f32 = _IN_DT[d.in_dtype], torch.float32
-    total, H, P, N, G = int(x.shape[0]), d.nheads, d.head_dim, d.d_state, d.ngroups
-    args = [_arg(cu_seqlens, torch.int32, (d.batch + 1,), "cu_seqlens"), _arg(x, in_dt, (total, H, P), "x"),
-            _arg(B, in_dt, (total, G, N), "B"), _arg(C, in_dt, (total, G, N), "C"), _arg(dt, f32, (total, H), "dt"),
-            _arg(A, f32, (H,), "A"), _arg(D, f32, (H,), "D"), _arg(y, f32, (total, H, P), "y")]
-    if state.pos.device != x.device:
-        raise ValueError(f"the state is on {state.pos.device}, x on {x.device}")
+    a, in_dt, f32, dev = _arg, _IN_DT[d.in_dtype], torch.float32, _device(x, "x")
+    total, H, P, N, G = x.shape[0], d.nheads, d.head_dim, d.d_state, d.ngroups
+    if state.pos.get_device() != dev:
+        raise ValueError(f"the state is on {state.pos.device}, the current device is cuda:{dev}")
+    args = (a(cu_seqlens, torch.int32, (d.batch + 1,), "cu_seqlens", dev), a(x, in_dt, (total, H, P), "x", dev),
+            a(B, in_dt, (total, G, N), "B", dev), a(C, in_dt, (total, G, N), "C", dev), a(dt, f32, (total, H), "dt", dev),
+            a(A, f32, (H,), "A", dev), a(D, f32, (H,), "D", dev), a(y, f32, (total, H, P), "y", dev))
     if workspace is None:
         need = rssm_prefill_scan_workspace_bytes(d, total, max_seqlen)
         if need:
@@ -303,7 +315,7 @@ def rssm_prefill_scan(state, cu_seqlens, max_seqlen, x, B, C, dt, A, D, y, works
             if stream is not None:
                 workspace.record_stream(stream)
     size = 0 if workspace is None else workspace.numel()
-    ws = _arg(workspace, torch.uint8, (size,), "workspace")
+    ws = a(workspace, torch.uint8, (size,), "workspace", dev)
     _check(lib().rssm_prefill_scan(ct.byref(d), ct.byref(state.struct), total, int(max_seqlen), *args, ws, size,
                                    _stream(stream)), "rssm_prefill_scan")
     return y

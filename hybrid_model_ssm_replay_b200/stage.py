@@ -106,29 +106,29 @@ def rssm_stage_conv_prompt(desc, cu_seqlens, zxbcdt, conv_state, conv_w, conv_b,
                            stream=None):
     """rssm_stage_conv for every token of packed prompts; conv_state is read
     and updated. err: the state's error word (RssmState.err), or None."""
-    a, bf, f32 = rssm._arg, torch.bfloat16, torch.float32
+    a, bf, f32, dev = rssm._arg, torch.bfloat16, torch.float32, rssm._device(zxbcdt, "zxbcdt")
     H, P, N, G = desc.nheads, desc.head_dim, desc.d_state, desc.ngroups
-    total, chans = int(zxbcdt.shape[0]), H * P + 2 * G * N
+    total, chans = zxbcdt.shape[0], H * P + 2 * G * N
     rssm._check(_lib().rssm_stage_conv_prompt(
-        ct.byref(desc), total, a(cu_seqlens, torch.int32, (desc.batch + 1,), "cu_seqlens"),
-        a(zxbcdt, bf, (total, H * P + chans + H), "zxbcdt"), a(conv_state, bf, (desc.batch, 3, chans), "conv_state"),
-        a(conv_w, f32, (chans, 4), "conv_w"), a(conv_b, f32, (chans,), "conv_b"), a(dt_bias, f32, (H,), "dt_bias"),
-        a(x, bf, (total, H, P), "x"), a(B, bf, (total, G, N), "B"), a(C, bf, (total, G, N), "C"),
-        a(dt, f32, (total, H), "dt"), a(err, torch.int32, (1,), "err"), rssm._stream(stream)),
+        ct.byref(desc), total, a(cu_seqlens, torch.int32, (desc.batch + 1,), "cu_seqlens", dev),
+        a(zxbcdt, bf, (total, H * P + chans + H), "zxbcdt", dev),
+        a(conv_state, bf, (desc.batch, 3, chans), "conv_state", dev), a(conv_w, f32, (chans, 4), "conv_w", dev),
+        a(conv_b, f32, (chans,), "conv_b", dev), a(dt_bias, f32, (H,), "dt_bias", dev),
+        a(x, bf, (total, H, P), "x", dev), a(B, bf, (total, G, N), "B", dev), a(C, bf, (total, G, N), "C", dev),
+        a(dt, f32, (total, H), "dt", dev), a(err, torch.int32, (1,), "err", dev), rssm._stream(stream)),
         "rssm_stage_conv_prompt")
 
 
 def rssm_stage_gate_norm_prompt(desc, y, zxbcdt, norm_w, eps, out, stream=None):
-    """rssm_stage_gate_norm for every row of packed prompts (desc's batch is not used)."""
-    a, bf, f32 = rssm._arg, torch.bfloat16, torch.float32
+    """rssm_stage_gate_norm for every row of packed prompts (desc's batch is
+    not used); y [rows][d_inner] or [rows][H][P]."""
+    a, bf, f32, dev = rssm._arg, torch.bfloat16, torch.float32, rssm._device(zxbcdt, "zxbcdt")
     H, P = desc.nheads, desc.head_dim
-    rows, din = int(zxbcdt.shape[0]), H * P
-    if tuple(y.shape) != (rows, din):
-        y = y.reshape(-1, din) if y.is_contiguous() and y.dim() == 3 and y.shape[1:] == (H, P) else y
+    rows, din = zxbcdt.shape[0], H * P
     rssm._check(_lib().rssm_stage_gate_norm_prompt(
-        ct.byref(desc), rows, a(y, f32, (rows, din), "y"),
-        a(zxbcdt, bf, (rows, 2 * din + 2 * desc.ngroups * desc.d_state + H), "zxbcdt"),
-        a(norm_w, f32, (din,), "norm_w"), float(eps), a(out, bf, (rows, din), "out"), rssm._stream(stream)),
+        ct.byref(desc), rows, a(y, f32, (rows, din) if y.dim() == 2 else (rows, H, P), "y", dev),
+        a(zxbcdt, bf, (rows, 2 * din + 2 * desc.ngroups * desc.d_state + H), "zxbcdt", dev),
+        a(norm_w, f32, (din,), "norm_w", dev), float(eps), a(out, bf, (rows, din), "out", dev), rssm._stream(stream)),
         "rssm_stage_gate_norm_prompt")
     return out
 
@@ -137,15 +137,18 @@ def rssm_stage_add_norm(u, v, pre_w, eps, out, post_w=None, gate=None, scale=1.0
     """u_out = u + scale * gate * norm(v, post_w); out = norm(u_out, pre_w).
     u_out None: u itself is updated. v None: the norm of u alone (u_out then
     receives a copy, if it is given). pre_w and out None: no norm."""
-    a, bf, f32 = rssm._arg, torch.bfloat16, torch.float32
-    rows, dim = (int(n) for n in u.shape)
-    dt = u.dtype if u.dtype in (bf, f32) else (bf, f32)
-    up = a(u, dt, (rows, dim), "u")
-    uo = (None if v is None else up) if u_out is None else a(u_out, dt, (rows, dim), "u_out")
+    a, bf, f32, dev = rssm._arg, torch.bfloat16, torch.float32, rssm._device(u, "u")
+    if u.dim() != 2:
+        raise ValueError(f"u has shape {tuple(u.shape)}, expected rows of one width")
+    shape, wide = u.shape, u.shape[1:]
+    t = f32 if u.dtype == f32 else bf
+    up = a(u, t, shape, "u", dev)
+    uo = (None if v is None else up) if u_out is None else a(u_out, t, shape, "u_out", dev)
     rssm._check(_lib().rssm_stage_add_norm(
-        rows, dim, rssm.RSSM_F32 if u.dtype == f32 else rssm.RSSM_BF16, up, a(v, bf, (rows, dim), "v"),
-        a(post_w, f32, (dim,), "post_w"), a(gate, f32, (dim,), "gate"), float(scale), a(pre_w, f32, (dim,), "pre_w"),
-        float(eps), uo, a(out, bf, (rows, dim), "out"), rssm._stream(stream)), "rssm_stage_add_norm")
+        shape[0], shape[1], rssm.RSSM_F32 if t == f32 else rssm.RSSM_BF16, up, a(v, bf, shape, "v", dev),
+        a(post_w, f32, wide, "post_w", dev), a(gate, f32, wide, "gate", dev), float(scale),
+        a(pre_w, f32, wide, "pre_w", dev), float(eps), uo, a(out, bf, shape, "out", dev), rssm._stream(stream)),
+        "rssm_stage_add_norm")
     return out
 
 

@@ -115,7 +115,7 @@ def test_bindings_refuse_cpu_tensors_and_wrong_types():
     with pytest.raises(ValueError):
         stage.rssm_stage_add_norm(t, t.bfloat16(), t[0], 1e-5, t.bfloat16())
     with pytest.raises(ValueError):
-        rssm._arg(t, torch.float32, (4, 8), "t")
+        rssm._arg(t, torch.float32, (4, 8), "t", 0)
 
 
 def test_stage_prefill_needs_the_replay_scheme():
