@@ -572,7 +572,7 @@ __global__ void __launch_bounds__(kSuThreads, 2)
 #pragma unroll
                 for (int j = 7; j >= 0; --j) {
                     const float ds = __shfl_sync(0xffffffffu, d, j, 8);
-                    if ((lane & 7) > j) run = fmaf(A2, dnx, run);
+                    run = (lane & 7) > j ? fmaf(A2, dnx, run) : run;
                     dnx = ds;
                     own[j] = ds * su_exp2(run);
                 }
@@ -629,15 +629,17 @@ uint32_t vv[2][16];
                     }
                     if (k == 0) su_wait_ld();
                     if (J == q) {
+                        // selections, not branches: every lane goes another way
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
                             const int c = 16 * k + 2 * i;
-                            float2 w = m[i];
-                            if (oct == (c >> 3)) w = make_float2(own[c & 7], own[(c & 7) + 1]);
-                            m[i].x = lane >= c ? __uint_as_float(v[2 * i]) * w.x : 0.f;
-                            m[i].y = lane > c ? __uint_as_float(v[2 * i + 1]) * w.y : 0.f;
-                            if (lane == c) m[i].x += Dh;  // D x_t
-                            if (lane == c + 1) m[i].y += Dh;
+                            const bool eq = oct == (c >> 3);
+                            const float wx = eq ? own[c & 7] : m[i].x, wy = eq ? own[(c & 7) + 1] : m[i].y;
+                            const float dx = lane == c ? Dh : 0.f, dy = lane == c + 1 ? Dh : 0.f;  // D x_t
+                            const float ex = fmaf(__uint_as_float(v[2 * i]), wx, dx);
+                            const float ey = fmaf(__uint_as_float(v[2 * i + 1]), wy, dy);
+                            m[i].x = lane >= c ? ex : 0.f;
+                            m[i].y = lane > c ? ey : 0.f;
                         }
                     } else {
 #pragma unroll

@@ -58,7 +58,7 @@ struct ConvPromptArgs {
 };
 
 // silu as rssm_stage_conv forms it, in bf16.
-__device__ __noinline__ uint16_t silu_exact(float o) {
+__device__ __forceinline__ uint16_t silu_exact(float o) {
     return __bfloat16_as_ushort(__float2bfloat16_rn(o / (1.0f + expf(-o))));
 }
 
@@ -100,21 +100,22 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 
 // silu of two channels as a pair of bf16, the bits of silu_exact for less:
 // o / (1 + 2^(-o log2 e)) with the approximate exponential and one
-// approximate reciprocal of both denominators' product, 1/a = b rcp(a b).
-// For |o| < 32 that is within 26 fp32 spacings of the quotient (19 from the
+// approximate reciprocal r of both denominators' product, 1/a = b r. For
+// o > -32 that is within 26 fp32 spacings of the quotient (19 from the
 // argument -o log2 e, up to 46 in size, 2 of ex2, 1 of rcp, 4 of the add and
-// the products) and the library form within 3, so both round to the same
-// bf16 unless the value lies within 32 spacings of the middle between two
-// bf16: one value in a thousand, which takes the library form.
+// the products) and the library form within 3. So when 1 - 2^-18 and 1 + 2^-18
+// times it round to the same bf16, the library form does too; else (one value
+// in a thousand), and when r is NaN or so small that an o may be below -32,
+// the library form decides.
 __device__ __forceinline__ uint32_t silu2(float2 o) {
     const float2 t = mul2(o, make_float2(-1.4426950408889634f, -1.4426950408889634f));
     const float2 d = add2(make_float2(ex2_approx(t.x), ex2_approx(t.y)), make_float2(1.0f, 1.0f));
     const float r = rcp_approx(d.x * d.y);
     const float2 v = mul2(o, mul2(make_float2(d.y, d.x), make_float2(r, r)));
-    uint32_t w = pack_bf16(v.x, v.y);
-    const uint32_t o0 = (__float_as_uint(v.x) - (0x8000u - 32u)) & 0xFFFFu;
-    const uint32_t o1 = (__float_as_uint(v.y) - (0x8000u - 32u)) & 0xFFFFu;
-    if (!(min(o0, o1) > 64u && fmaxf(fabsf(o.x), fabsf(o.y)) < 32.0f))
+    constexpr float kUp = 1.0f + 1.0f / 262144.0f, kDown = 1.0f - 1.0f / 262144.0f;
+    const float2 lo = mul2(v, make_float2(kDown, kDown)), hi = mul2(v, make_float2(kUp, kUp));
+    uint32_t w = pack_bf16(lo.x, lo.y);
+    if (!(r > 1.4210854715202004e-14f) || w != pack_bf16(hi.x, hi.y))  // 2^-46
         w = silu_exact(o.x) | (static_cast<uint32_t>(silu_exact(o.y)) << 16);
     return w;
 }
@@ -151,14 +152,12 @@ __device__ __forceinline__ int first_request(const int32_t* cu, int batch, int t
 // What a thread of k_conv_prompt has of its channels: VEC as one load brings
 // them, as floats, and the products.
 template <int VEC> struct Chans;
-template <> struct Chans<8> {
-    using Raw = uint4;
-    float2 f[4];
+template <> struct Chans<4> {
+    using Raw = uint2;
+    float2 f[2];
     __device__ __forceinline__ void set(const Raw& u) {
         f[0] = make_float2(bf_lo(u.x), bf_hi(u.x));
         f[1] = make_float2(bf_lo(u.y), bf_hi(u.y));
-        f[2] = make_float2(bf_lo(u.z), bf_hi(u.z));
-        f[3] = make_float2(bf_lo(u.w), bf_hi(u.w));
     }
 };
 template <> struct Chans<1> {
@@ -168,7 +167,7 @@ template <> struct Chans<1> {
 };
 
 template <int VEC>
-__global__ void __launch_bounds__(kConvThreads, 2) k_conv_prompt(const ConvPromptArgs a) {
+__global__ void __launch_bounds__(kConvThreads, 4) k_conv_prompt(const ConvPromptArgs a) {
     using Raw = typename Chans<VEC>::Raw;
     constexpr int kPairs = (VEC + 1) / 2;
     constexpr int kAhead = 4;  // rows fetched before the ones at work
@@ -248,35 +247,55 @@ __global__ void __launch_bounds__(kConvThreads, 2) k_conv_prompt(const ConvPromp
             r1.set(row(from - 2));
             r2.set(row(from - 1));
         }
+        const __nv_bfloat16* from_x = in + static_cast<size_t>(from) * Dp;   // the next row to fetch
+        __nv_bfloat16* to_y = dst + static_cast<size_t>(from) * width;      // the next token's results
         Raw next[kAhead];
 #pragma unroll
         for (int k = 0; k < kAhead; ++k)
-            if (from + k < to) next[k] = row(from + k);
-        for (int t = from; t < to; t += kAhead) {
+            if (from + k < to) {
+                next[k] = *reinterpret_cast<const Raw*>(from_x);
+                from_x += Dp;
+            }
+        auto token = [&](const Raw& raw) {
+            Chans<VEC> cur;
+            cur.set(raw);
+            uint32_t y[kPairs];
+#pragma unroll
+            for (int i = 0; i < kPairs; ++i) {
+                float2 o = fma2(w[0][i], r0.f[i], bias[i]);
+                o = fma2(w[1][i], r1.f[i], o);
+                o = fma2(w[2][i], r2.f[i], o);
+                o = fma2(w[3][i], cur.f[i], o);
+                y[i] = silu2(o);
+            }
+            if constexpr (VEC == 4)
+                *reinterpret_cast<uint2*>(to_y) = make_uint2(y[0], y[1]);
+            else
+                *reinterpret_cast<uint16_t*>(to_y) = static_cast<uint16_t>(y[0]);
+            to_y += width;
+            r0 = r1;
+            r1 = r2;
+            r2 = cur;
+        };
+        int left = to - from;
+#pragma unroll 1
+        for (; left >= 2 * kAhead; left -= kAhead)
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) {
-                if (t + k >= to) break;
-                Chans<VEC> cur;
-                cur.set(next[k]);
-                if (t + kAhead + k < to) next[k] = row(t + kAhead + k);
-                uint32_t y[kPairs];
-#pragma unroll
-                for (int i = 0; i < kPairs; ++i) {
-                    float2 o = fma2(w[0][i], r0.f[i], bias[i]);
-                    o = fma2(w[1][i], r1.f[i], o);
-                    o = fma2(w[2][i], r2.f[i], o);
-                    o = fma2(w[3][i], cur.f[i], o);
-                    y[i] = silu2(o);
-                }
-                __nv_bfloat16* to_y = dst + static_cast<size_t>(t + k) * width;
-                if constexpr (VEC == 8)
-                    *reinterpret_cast<uint4*>(to_y) = make_uint4(y[0], y[1], y[2], y[3]);
-                else
-                    *reinterpret_cast<uint16_t*>(to_y) = static_cast<uint16_t>(y[0]);
-                r0 = r1;
-                r1 = r2;
-                r2 = cur;
+                const Raw raw = next[k];
+                next[k] = *reinterpret_cast<const Raw*>(from_x);
+                from_x += Dp;
+                token(raw);
             }
+        left -= kAhead;  // rows not yet fetched
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+            if (k < left + kAhead) token(next[k]);
+#pragma unroll 1
+        for (; left > 0; --left) {
+            const Raw raw = *reinterpret_cast<const Raw*>(from_x);
+            from_x += Dp;
+            token(raw);
         }
     }
 }
@@ -668,19 +687,20 @@ rssm_status_t rssm_stage_conv_prompt(const rssm_desc_t* d, int32_t total, const 
     a.C = static_cast<__nv_bfloat16*>(C);
     a.dt = dt;
     a.err = err;
-    // 16-byte accesses when every row and each of x, B, C starts on 16 bytes
+    // four channels at a time when every row and each of x, B, C starts on 8 bytes
     const int chans = a.din + 2 * a.gn;
-    const bool vec = a.din % 8 == 0 && a.gn % 8 == 0 && a.H % 8 == 0;
-    const int per_cta = (vec ? 8 : 1) * kConvThreads;
+    const bool vec = a.din % 4 == 0 && a.gn % 4 == 0 && a.H % 4 == 0;
+    const int per_cta = (vec ? 4 : 1) * kConvThreads;
     const int ny = (chans + per_cta - 1) / per_cta + 1;  // and the dt heads
     if (ny > 65535) return RSSM_ERR_SHAPE;
-    // Tokens per CTA: 32 (three rows before them are read again), fewer while
-    // that leaves SMs without work
-    a.tok = 32;
+    // Tokens per CTA: 128 (three rows before them are read again, and the
+    // weights once per CTA; 778 us at 32, 714 us at 128 for 256 x 512 tokens),
+    // fewer while that leaves SMs without work
+    a.tok = 128;
     while (a.tok > 4 && static_cast<long long>((total - 1) / a.tok + 1) * ny < 4ll * sm_count()) a.tok /= 2;
     const dim3 grid(static_cast<unsigned>((total - 1) / a.tok + 1), static_cast<unsigned>(ny));
     if (vec)
-        k_conv_prompt<8><<<grid, kConvThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
+        k_conv_prompt<4><<<grid, kConvThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
     else
         k_conv_prompt<1><<<grid, kConvThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
     return launched();
