@@ -207,8 +207,9 @@ __global__ void __launch_bounds__(kThreads) k_scan(const ScanArgs a) {
 // scaled, with D x added, before Y takes its place in tensor memory; U takes
 // M's. 112 KB of shared memory: C, B, x, and one buffer that holds the parts
 // of h and then, with half of C's (read by then), of w x. Each part of the
-// next block is fetched (TMA) as soon as its buffer has been read. Rows past
-// the request's end are zeroed in x and B.
+// next block is fetched (TMA) as soon as its buffer has been read; x's buffer
+// takes the outputs to memory first. Rows past the request's end are zeroed
+// in x and B.
 //
 // Decays. No difference of two sums of dt is formed: between two tokens of
 // the same 8 the exponent of M is the running sum of dt from s + 1 to t, and
@@ -228,7 +229,8 @@ __global__ void __launch_bounds__(kThreads) k_scan(const ScanArgs a) {
 // ---------------------------------------------------------------------------
 constexpr int kSuTok = 128;                    // tokens per block
 constexpr int kSuThreads = 256;
-constexpr int kSuIssuer = 4;                   // a warp with none of M's lower triangle
+constexpr int kSuIssuer = 4;                   // two warps with none of M's lower triangle: of the products
+constexpr int kSuStorer = 5;                   // and of the second half of Y
 constexpr uint32_t kSuBlk = kSuTok * 128u;     // 128 rows of 128 bytes, swizzled: 16 KB
 constexpr uint32_t kSuB = 0;                   // B rows, two 64-column blocks
 constexpr uint32_t kSuX = 2 * kSuBlk;          // x rows
@@ -237,8 +239,8 @@ constexpr uint32_t kSuC1 = 5 * kSuBlk;         // C columns 64.. ; later w x lo 
 constexpr uint32_t kSuC0 = 6 * kSuBlk;         // C columns 0..63
 constexpr uint32_t kSuCol = 7 * kSuBlk;        // float [128]: dt_s exp(decay from s + 1 to the end of its 8 tokens)
 constexpr uint32_t kSuSum = kSuCol + 512;      // float [16]: dt sums of 8 tokens each
-constexpr uint32_t kSuBar = kSuSum + 64;       // 5 mbarriers, tensor-memory address
-constexpr uint32_t kSuSmem = kSuBar + 48;
+constexpr uint32_t kSuBar = kSuSum + 64;       // 7 mbarriers, tensor-memory address
+constexpr uint32_t kSuSmem = kSuBar + 64;
 constexpr uint32_t kSuCols = 256;              // tensor-memory columns
 constexpr uint32_t kTmS = 0, kTmLo = 128, kTmY = 192;  // S, then M hi, mid; M lo; O, then Y (U: 0..191)
 
@@ -397,6 +399,15 @@ __device__ __forceinline__ void su_prefetch(const CUtensorMap& map, int x, int y
     asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global [%0, {%1, %2}];" ::"l"(&map), "r"(x), "r"(y) : "memory");
 }
 
+// A bounded wait for phase `parity`; the loop of the rare long wait is kept
+// out of the kernel's body, which is long enough for the instruction cache.
+__device__ __noinline__ bool su_wait_long(uint32_t bar, uint32_t parity) {
+    return mbar_wait_bounded(bar, parity, kWaitNs);
+}
+__device__ __forceinline__ bool su_wait(uint32_t bar, uint32_t parity) {
+    return mbar_try_wait(bar, parity, 100000u) || su_wait_long(bar, parity);
+}
+
 template <bool OUT>
 __global__ void __launch_bounds__(kSuThreads, 2)
     k_scan_umma(const ScanArgs a, const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mb,
@@ -416,28 +427,31 @@ __global__ void __launch_bounds__(kSuThreads, 2)
         return;
     }
     const uint32_t bar_in = sb + kSuBar, bar_s = bar_in + 8, bar_o = bar_in + 16, bar_y = bar_in + 24,
-                   bar_u = bar_in + 32;
-    volatile uint32_t* s_tmem = reinterpret_cast<volatile uint32_t*>(smem + kSuBar + 40);
+                   bar_u = bar_in + 32, bar_x = bar_in + 40, bar_f = bar_in + 48;
+    volatile uint32_t* s_tmem = reinterpret_cast<volatile uint32_t*>(smem + kSuBar + 56);
     const bool wide = N > 64;  // B and C have a second block of 64 columns
-    const uint32_t in_bytes = kSuBlk * (1 + (wide ? 2u : 1u) * (OUT ? 2u : 1u));
+    const uint32_t in_bytes = kSuBlk * (wide ? 2u : 1u) * (OUT ? 2u : 1u);  // B and C
     const int xx = h * P + p0, bx = g * N;
     const bool issuer = warp == kSuIssuer;  // its elected lane issues every copy and product
     auto load_c0 = [&](int t) { su_tma(sb + kSuC0, mc, bx, t, bar_in); };
-    auto load_x = [&](int t) { su_tma(sb + kSuX, mx, xx, t, bar_in); };
+    auto load_x = [&](int t) {
+        mbar_expect_tx(bar_x, kSuBlk);
+        su_tma(sb + kSuX, mx, xx, t, bar_x);
+    };
     auto load_bc = [&](int t) {
         su_tma(sb + kSuB, mb, bx, t, bar_in);
         if (wide) su_tma(sb + kSuB + kSuBlk, mb, bx + 64, t, bar_in);
         if (OUT && wide) su_tma(sb + kSuC1, mc, bx + 64, t, bar_in);
     };
     if (issuer && elect_one()) {
-        for (int i = 0; i < 5; ++i) mbar_init(bar_in + 8 * i, 1);
+        for (int i = 0; i < 7; ++i) mbar_init(bar_in + 8 * i, 1);
         mbar_expect_tx(bar_in, in_bytes);
         if (OUT) load_c0(it.t0);
         load_x(it.t0);
         load_bc(it.t0);
     }
     if (warp == 0) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sb + kSuBar + 40),
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sb + kSuBar + 56),
                      "r"(kSuCols)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -507,11 +521,9 @@ __global__ void __launch_bounds__(kSuThreads, 2)
     for (int t0 = it.t0; t0 < it.t1; t0 += kSuTok, par ^= 1) {
         const bool more = t0 + kSuTok < it.t1;
         const float dn = more ? load_dt(t0 + kSuTok) : 0.f;
-        if (!mbar_wait_bounded(bar_in, par, kWaitNs)) timed_out = true;
+        if (!su_wait(bar_in, par)) timed_out = true;
         if (!more && t0 + row >= it.t1) {  // rows of the next request, or of none
             const uint4 zero = make_uint4(0, 0, 0, 0);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) *chunk(kSuX, 4 * half + j) = zero;
             if (wide || half == 0)
 #pragma unroll
                 for (int j = 0; j < 8; ++j) *chunk(kSuB + half * kSuBlk, j) = zero;
@@ -520,23 +532,28 @@ __global__ void __launch_bounds__(kSuThreads, 2)
         su_fence_before();
         if (__syncthreads_or(timed_out)) break;  // the block, its decays and the state's parts are in place
         su_fence_after();
+        if (OUT && warp == kSuStorer && t0 != it.t0) {
+            if (elect_one()) {  // Y of the block before has left x's buffer
+                asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                load_x(t0);
+            }
+            __syncwarp();
+        }
         if (OUT && issuer) {
             const uint64_t dB = su_desc(sb + kSuB), dR = su_desc(sb + kSuR);
             const uint64_t dC0 = su_desc(sb + kSuC0), dC1 = su_desc(sb + kSuC1);
             if (elect_one()) {
-#pragma unroll
-                for (int ks = 0; ks < 8; ++ks)
-                    if (16 * ks < N)
-                        su_mma<su_idesc(128, 0, 0)>(tm + kTmS, (ks < 4 ? dC0 : dC1) + 2 * (ks & 3),
-                                                    dB + (ks < 4 ? 0 : kSuBlk / 16) + 2 * (ks & 3), ks > 0);
+#pragma unroll 1
+                for (int ks = 0; ks < N / 16; ++ks)
+                    su_mma<su_idesc(128, 0, 0)>(tm + kTmS, (ks < 4 ? dC0 : dC1) + 2 * (ks & 3),
+                                                dB + (ks >> 2) * (kSuBlk / 16) + 2 * (ks & 3), ks > 0);
                 su_commit(bar_s);
-#pragma unroll
-                for (int ks = 0; ks < 8; ++ks)
-                    if (16 * ks < N) {
-                        const uint64_t c = (ks < 4 ? dC0 : dC1) + 2 * (ks & 3);
-                        su_mma<su_idesc(64, 0, 1)>(tm + kTmY, c, dR + 128 * ks, ks > 0);
-                        su_mma<su_idesc(64, 0, 1)>(tm + kTmY, c, dR + kSuBlk / 16 + 128 * ks, 1);
-                    }
+#pragma unroll 1
+                for (int ks = 0; ks < N / 16; ++ks) {
+                    const uint64_t c = (ks < 4 ? dC0 : dC1) + 2 * (ks & 3);
+                    su_mma<su_idesc(64, 0, 1)>(tm + kTmY, c, dR + 128 * ks, ks > 0);
+                    su_mma<su_idesc(64, 0, 1)>(tm + kTmY, c, dR + kSuBlk / 16 + 128 * ks, 1);
+                }
                 su_commit(bar_o);
                 if (more) {  // the next block on its way to L2
                     su_prefetch(mx, xx, t0 + kSuTok);
@@ -560,104 +577,115 @@ __global__ void __launch_bounds__(kSuThreads, 2)
                                                    (static_cast<size_t>(t0 + s) * H + h) * P + p0 + 8 * j);
         };
         if (OUT) {
-            // dt sums from the start of this thread's token's 32-block to the token,
-            // of the 32-blocks before, and of those between J and it
+            // dt sums from the start of this thread's token's 32-block to the token
+            // and of the 32-blocks before
             const float4 mine = s_sum[q];
             const float pre32 = pre + ((oct > 0 ? mine.x : 0.f) + (oct > 1 ? mine.y : 0.f) + (oct > 2 ? mine.z : 0.f));
             const float before = (q > 0 ? sums.x : 0.f) + (q > 1 ? sums.y : 0.f) + (q > 2 ? sums.z : 0.f);
-            // the same 8 tokens' factors, from the running sum: A2 times the dt sum from s + 1 to t
-            float own[8];
-            if ((q >> 1) == half) {
+            // M over S, 32-blocks 2 half and 2 half + 1 of its columns, 16 at a
+            // time: hi and mid parts in the columns read, lo in its own
+            auto put_m = [&](int J, int k, const float2 (&m)[8]) {
+                uint32_t hi[8], mid[8], lo[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) split3(m[i], hi[i], mid[i], lo[i]);
+                su_st8(tml + kTmS + 32 * J + 16 * k, hi);
+                su_st8(tml + kTmS + 32 * J + 16 * k + 8, mid);
+                su_st8(tml + kTmLo + 16 * J + 8 * k, lo);
+            };
+            // column factors of columns 16 k .. of 32-block J; f0, f1: decay from the
+            // end of their two groups of 8 to this token
+            auto factors = [&](int J, int k, float f0, float f1, float2 (&m)[8]) {
+                const float4* c4 = reinterpret_cast<const float4*>(s_col + 32 * J + 16 * k);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float4 c = c4[i];
+                    const float2 f2 = i < 2 ? make_float2(f0, f0) : make_float2(f1, f1);
+                    m[2 * i] = mul2(f2, make_float2(c.x, c.y));
+                    m[2 * i + 1] = mul2(f2, make_float2(c.z, c.w));
+                }
+            };
+            if ((q >> 1) == half) {  // the block on the diagonal
+                // the same 8 tokens' factors, from the running sum: A2 times the dt
+                // sum from s + 1 to t; zero for later tokens
+                uint32_t own[8];
+                const int l7 = lane & 7;
                 float run = 0.f, dnx = 0.f;
 #pragma unroll
                 for (int j = 7; j >= 0; --j) {
                     const float ds = __shfl_sync(0xffffffffu, d, j, 8);
-                    run = (lane & 7) > j ? fmaf(A2, dnx, run) : run;
+                    run = fmaf(A2, l7 > j ? dnx : 0.f, run);
                     dnx = ds;
-                    own[j] = ds * su_exp2(run);
+                    own[j] = __float_as_uint(ds * su_exp2(run)) & static_cast<uint32_t>(~((l7 - j) >> 31));
                 }
+                if (!su_wait(bar_s, par)) timed_out = true;
+                su_fence_after();
+#pragma unroll 1
+                for (int k = 0; k < 2; ++k) {
+                    uint32_t v[16];
+                    su_ld16(tml + kTmS + 32 * q + 16 * k, v);
+                    const float z2 = oct > 2 ? mine.z : 0.f, y2 = (oct > 1 ? mine.y : 0.f) + z2;
+                    float2 m[8];
+                    factors(q, k, su_exp2(A2 * (pre + (k ? 0.f : y2))), su_exp2(A2 * (pre + (k ? 0.f : z2))), m);
+                    su_wait_ld();
+                    // by masks, not branches: every lane goes another way (S and the
+                    // factor of a later token may be NaN)
+#pragma unroll
+                    for (int o = 0; o < 2; ++o) {
+                        const uint32_t eq = oct == 2 * k + o ? ~0u : 0u, gt = oct > 2 * k + o ? ~0u : 0u;
+                        const uint32_t De = __float_as_uint(Dh) & eq;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const int i = 4 * o + j / 2;
+                            const uint32_t w = (own[j] & eq) | (__float_as_uint(j & 1 ? m[i].y : m[i].x) & gt);
+                            const uint32_t seen = gt | (eq & static_cast<uint32_t>(~((l7 - j) >> 31)));
+                            const uint32_t dx = l7 == j ? De : 0u;  // D x_t
+                            const float e = fmaf(__uint_as_float(v[8 * o + j] & seen), __uint_as_float(w),
+                                                 __uint_as_float(dx));
+                            if (j & 1)
+                                m[i].y = e;
+                            else
+                                m[i].x = e;
+                        }
+                    }
+                    put_m(q, k, m);
+                }
+            } else {
+                if (!su_wait(bar_s, par)) timed_out = true;
+                su_fence_after();
             }
-            if (!mbar_wait_bounded(bar_s, par, kWaitNs)) timed_out = true;
-            su_fence_after();
-            // M over S, 32-blocks 2 half and 2 half + 1 of its columns, 16 at a
-            // time: hi and mid parts in the columns read, lo in its own
 #pragma unroll 1
             for (int J = 2 * half; J < 2 * half + 2; ++J) {
-                const uint32_t tS = tml + kTmS + 32 * J, tL = tml + kTmLo + 16 * J;
+                if (J == q) continue;
                 if (J > q) {  // nothing but later tokens
                     const uint32_t zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        su_st8(tS + 16 * k, zero);
-                        su_st8(tS + 16 * k + 8, zero);
-                        su_st8(tL + 8 * k, zero);
+                        su_st8(tml + kTmS + 32 * J + 16 * k, zero);
+                        su_st8(tml + kTmS + 32 * J + 16 * k + 8, zero);
+                        su_st8(tml + kTmLo + 16 * J + 8 * k, zero);
                     }
                     continue;
                 }
-                // decay from the end of each 8 tokens of the columns to this thread's token
                 const float4 o = s_sum[J];
-                float to = pre32;  // from the end of the 32-block
-                if (J == q) to = pre;
-                if (J < 1 && q > 1) to += sums.y;
-                if (J < 2 && q > 2) to += sums.z;
-                float f[4];
-                if (J == q) {  // (of columns of its own 8 tokens or later ones: not used)
-                    f[0] = su_exp2(A2 * (to + ((oct > 1 ? o.y : 0.f) + (oct > 2 ? o.z : 0.f))));
-                    f[1] = su_exp2(A2 * (to + (oct > 2 ? o.z : 0.f)));
-                    f[2] = su_exp2(A2 * to);
-                    f[3] = 0.f;
-                } else {
-                    f[3] = su_exp2(A2 * to);
-                    f[2] = su_exp2(A2 * (to + o.w));
-                    f[1] = su_exp2(A2 * (to + (o.z + o.w)));
-                    f[0] = su_exp2(A2 * (to + (o.y + o.z + o.w)));
-                }
-                const float4* c4 = reinterpret_cast<const float4*>(s_col + 32 * J);
-uint32_t vv[2][16];
-                    su_ld16(tS, vv[0]);
-                    su_ld16(tS + 16, vv[1]);
-#pragma unroll
+                const float to = pre32 + ((J < 1 && q > 1 ? sums.y : 0.f) + (J < 2 && q > 2 ? sums.z : 0.f));
+#pragma unroll 1
                 for (int k = 0; k < 2; ++k) {
-                    uint32_t (&v)[16] = vv[k];
+                    uint32_t v[16];
+                    su_ld16(tml + kTmS + 32 * J + 16 * k, v);
                     float2 m[8];
+                    factors(J, k, su_exp2(A2 * (to + (k ? o.w : o.y + o.z + o.w))),
+                            su_exp2(A2 * (to + (k ? 0.f : o.z + o.w))), m);
+                    su_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float4 c = c4[4 * k + i];
-                        const float2 f2 = make_float2(f[2 * k + i / 2], f[2 * k + i / 2]);
-                        m[2 * i] = mul2(f2, make_float2(c.x, c.y));
-                        m[2 * i + 1] = mul2(f2, make_float2(c.z, c.w));
-                    }
-                    if (k == 0) su_wait_ld();
-                    if (J == q) {
-                        // selections, not branches: every lane goes another way
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int c = 16 * k + 2 * i;
-                            const bool eq = oct == (c >> 3);
-                            const float wx = eq ? own[c & 7] : m[i].x, wy = eq ? own[(c & 7) + 1] : m[i].y;
-                            const float dx = lane == c ? Dh : 0.f, dy = lane == c + 1 ? Dh : 0.f;  // D x_t
-                            const float ex = fmaf(__uint_as_float(v[2 * i]), wx, dx);
-                            const float ey = fmaf(__uint_as_float(v[2 * i + 1]), wy, dy);
-                            m[i].x = lane >= c ? ex : 0.f;
-                            m[i].y = lane > c ? ey : 0.f;
-                        }
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            m[i] = mul2(m[i], make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])));
-                    }
-                    uint32_t hi[8], mid[8], lo[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) split3(m[i], hi[i], mid[i], lo[i]);
-                    su_st8(tS + 16 * k, hi);
-                    su_st8(tS + 16 * k + 8, mid);
-                    su_st8(tL + 8 * k, lo);
+                    for (int i = 0; i < 8; ++i)
+                        m[i] = mul2(m[i], make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])));
+                    put_m(J, k, m);
                 }
             }
             // the state's share of the outputs, scaled in place; Y is added to it
             const float fac = su_exp2(A2 * (before + pre32));
             const float2 fac2 = make_float2(fac, fac);
-            if (!mbar_wait_bounded(bar_o, par, kWaitNs)) timed_out = true;
+            if (!su_wait(bar_o, par)) timed_out = true;
             su_fence_after();
             {
                 uint32_t o[2][16];
@@ -684,14 +712,17 @@ uint32_t vv[2][16];
         // warps, and among the four warps of each q, which share a scheduler.
         const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
         __nv_bfloat162 z = zero;  // NaN when x has a NaN or infinity
-        constexpr uint64_t kFirst = OUT ? 0x1F180D041C160C00ull : 0x1C1814100C080400ull;  // byte w: warp w's first pass
-        constexpr uint32_t kPasses = OUT ? 0x14983214u : 0x44444444u;                      // digit w: how many
+        constexpr uint64_t kFirst = OUT ? 0x1E1A110E0B080500ull : 0x1C1814100C080400ull;  // byte w: warp w's first pass
+        constexpr uint32_t kPasses = OUT ? 0x24933335u : 0x44444444u;                      // digit w: how many
         const int first = static_cast<int>((kFirst >> (8 * warp)) & 31), passes = (kPasses >> (4 * warp)) & 15;
+        if (!su_wait(bar_x, par)) timed_out = true;
 #pragma unroll 1
         for (int pass = first; pass < first + passes; ++pass) {
             const int s = 4 * pass + (lane >> 3);
             const uint32_t at = static_cast<uint32_t>(128 * s + 16 * ((lane & 7) ^ (s & 7)));
-            const uint4 u = *reinterpret_cast<const uint4*>(smem + kSuX + at);
+            uint4* xp = reinterpret_cast<uint4*>(smem + kSuX + at);
+            uint4 u = *xp;
+            if (t0 + s >= it.t1) *xp = u = make_uint4(0, 0, 0, 0);  // a row of the next request, or of none
             // dt sums of the groups of 8 after the token's in its 32-block, and of the 32-blocks after
             const float4 o = s_sum[pass >> 3];
             const int so = (pass >> 1) & 3;
@@ -729,21 +760,31 @@ uint32_t vv[2][16];
             if (issuer) {
                 const uint64_t dX = su_desc(sb + kSuX);
                 if (elect_one()) {
-#pragma unroll
+#pragma unroll 1
                     for (int ks = 0; ks < kSuTok / 16; ++ks) {
                         su_mma_ts<su_idesc(64, 0, 1)>(tm + kTmY, tm + kTmS + 16 * ks, dX + 128 * ks, 1);
                         su_mma_ts<su_idesc(64, 0, 1)>(tm + kTmY, tm + kTmS + 16 * ks + 8, dX + 128 * ks, 1);
                         su_mma_ts<su_idesc(64, 0, 1)>(tm + kTmY, tm + kTmLo + 8 * ks, dX + 128 * ks, 1);
                     }
                     su_commit(bar_y);
+                    if (more) {
+                        mbar_expect_tx(bar_in, in_bytes);
+                        load_c0(t0 + kSuTok);
+                    }
                 }
                 __syncwarp();
             }
+        } else if (issuer) {
+            if (more && elect_one()) {
+                mbar_expect_tx(bar_in, in_bytes);
+                load_x(t0 + kSuTok);
+            }
+            __syncwarp();
         }
         d = dn;
         if (more) scan_dt();
         if (OUT) {
-            if (!mbar_wait_bounded(bar_y, par, kWaitNs)) timed_out = true;  // Y done, M and x read
+            if (!su_wait(bar_y, par)) timed_out = true;  // Y done, M and x read
             su_fence_after();
         }
         if (OUT && bad) {  // what was left out of Y, 8 columns at a time, before U takes M's place
@@ -782,57 +823,65 @@ uint32_t vv[2][16];
         if (issuer) {
             const uint64_t dB = su_desc(sb + kSuB), dR = su_desc(sb + kSuR);
             if (elect_one()) {
-#pragma unroll
+#pragma unroll 1
                 for (int ks = 0; ks < kSuTok / 16; ++ks)
                     su_mma<su_idesc(192, 1, 1)>(tm + kTmS, dB + 128 * ks, dR + 128 * ks, ks > 0);
                 su_commit(bar_u);
             }
             __syncwarp();
         }
-        if (OUT) {
-            // Y by way of the buffers of x and C's first half, 32 columns each
+        // Y leaves by way of x's buffer, 32 columns at a time: the first half at
+        // once, the second after the state has been brought up to date (and what
+        // is fetched into the buffer next, x, is needed last)
+        auto half_sync = [&]() {  // the four warps of this half
+            if (half == 0)
+                asm volatile("bar.sync 1, 128;" ::: "memory");
+            else
+                asm volatile("bar.sync 2, 128;" ::: "memory");
+        };
+        auto put_y = [&](int warp0) {
             uint32_t y[2][16];
             su_ld16(tml + kTmY + 32 * half, y[0]);
             su_ld16(tml + kTmY + 32 * half + 16, y[1]);
             su_wait_ld();
-            const uint32_t buf = half ? kSuC0 : kSuX;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const uint32_t* v = &y[i >> 2][4 * (i & 3)];
-                *chunk(buf, i) = make_uint4(v[0], v[1], v[2], v[3]);
+                *chunk(kSuX, i) = make_uint4(v[0], v[1], v[2], v[3]);
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncthreads();
+            half_sync();
             if (t0 + kSuTok <= it.t1) {
-                if (issuer && elect_one()) {
-                    su_tma_store(my, sb + kSuX, p0, h, t0);
-                    su_tma_store(my, sb + kSuC0, p0 + 32, h, t0);
-                    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-                    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                if (warp == warp0) {
+                    if (elect_one()) {
+                        if (pb < P) su_tma_store(my, sb + kSuX, pb, h, t0);
+                        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                    }
+                    __syncwarp();
                 }
             } else {  // not the rows of the next request: row by row
 #pragma unroll 1
                 for (int i = 0; i < 8; ++i) {
-                    const int r = 16 * i + 2 * warp + (lane >> 4), j = lane & 15;
-                    const uint4 v = *reinterpret_cast<const uint4*>(smem + (j < 8 ? kSuX : kSuC0) + r * 128 +
-                                                                    16 * ((j & 7) ^ (r & 7)));
-                    if (t0 + r < it.t1 && p0 + 4 * j < P)
-                        *reinterpret_cast<uint4*>(a.y + (static_cast<size_t>(t0 + r) * H + h) * P + p0 + 4 * j) = v;
+                    const int r = 16 * i + 4 * q + (lane >> 3), j = lane & 7;
+                    const uint4 v = *reinterpret_cast<const uint4*>(smem + kSuX + r * 128 + 16 * (j ^ (r & 7)));
+                    if (t0 + r < it.t1 && pb + 4 * j < P)
+                        *reinterpret_cast<uint4*>(a.y + (static_cast<size_t>(t0 + r) * H + h) * P + pb + 4 * j) = v;
                 }
+                half_sync();
             }
-        }
-        if (issuer) {
-            if (more && elect_one()) {
-                mbar_expect_tx(bar_in, in_bytes);
-                load_x(t0 + kSuTok);
-                if (OUT) load_c0(t0 + kSuTok);
-            }
-            __syncwarp();
-        }
-        if (!mbar_wait_bounded(bar_u, par, kWaitNs)) timed_out = true;
+        };
+        if (OUT && half == 0) put_y(0);
+        if (!su_wait(bar_u, par)) timed_out = true;
         su_fence_after();
         if (issuer) {
             if (more && elect_one()) load_bc(t0 + kSuTok);  // U has read B and the parts of w x
+            __syncwarp();
+        }
+        if (OUT && warp == 0) {
+            if (elect_one()) {
+                asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar_f) : "memory");
+            }
             __syncwarp();
         }
         const float dec = su_exp2(A2 * total);
@@ -854,6 +903,14 @@ uint32_t vv[2][16];
             }
         }
         if (OUT && more) put_state();
+        if (OUT && half == 1) {
+            if (!su_wait(bar_f, par)) timed_out = true;
+            put_y(kSuStorer);
+        }
+    }
+    if (OUT && warp == kSuStorer) {
+        if (elect_one()) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        __syncwarp();
     }
     if (timed_out) set_error(a.err, RSSM_DEVERR_TIMEOUT);
     if ((!OUT || it.last) && row < N) {
