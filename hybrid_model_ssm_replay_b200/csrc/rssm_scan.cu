@@ -109,23 +109,23 @@ __device__ __forceinline__ float* slot_dtsum(const ScanArgs& a, int slot, int h)
 // k_scan: the recurrence token by token, for every shape and both input
 // types. One CTA per (item, head); the state stays in registers, lane group
 // of N / 4 lanes per state row, 4 columns per lane, PASS rows per thread;
-// tokens are staged 16 at a time in shared memory as fp32.
+// tokens are staged 16 at a time in shared memory as fp32, the next ones
+// while these are worked on, and worked on 4 at a time: bound by the latency
+// of the row sums' shuffles otherwise. @KSCAN@
 // ---------------------------------------------------------------------------
 constexpr int kScanTok = 16;
 
 template <typename TIn, int PASS, bool OUT>
 __global__ void __launch_bounds__(kThreads) k_scan(const ScanArgs a) {
     extern __shared__ __align__(16) float sm[];
-    __shared__ float s_dt[kScanTok];
     const int H = a.s.H, P = a.s.P, N = a.s.N, G = a.s.G, lpr = a.s.lpr;
     const int h = blockIdx.x % H;
     Item it;
     if (!find_item<OUT>(a, blockIdx.x / H, it)) return;
     const int g = h / (H / G), tid = threadIdx.x;
-    float* s_x = sm;                          // [kScanTok][P]
-    float* s_y = s_x + kScanTok * P;          // [kScanTok][P]
-    float* s_B = s_y + kScanTok * P;          // [kScanTok][N]
-    float* s_C = s_B + kScanTok * N;          // [kScanTok][N]
+    // two buffers of [dt, decay | x | B | C] of kScanTok tokens, and the outputs
+    const int xs = (P + 3) & ~3, buf = kScanTok * (2 + xs + 2 * N);
+    float* s_y = sm + 2 * buf;  // [kScanTok][P]
     const int col = 4 * (tid & (lpr - 1)), row0 = tid / lpr, step = kThreads / lpr;
     const float* init = it.slot < 0 ? head_state(a, it.b, h) : slot_state(a, it.slot, h);
     float4 st[PASS];
@@ -139,37 +139,78 @@ __global__ void __launch_bounds__(kThreads) k_scan(const ScanArgs a) {
     const TIn* x = static_cast<const TIn*>(a.x);
     const TIn* B = static_cast<const TIn*>(a.B);
     const TIn* C = static_cast<const TIn*>(a.C);
-    float dtsum = 0.f;
-    for (int t0 = it.t0; t0 < it.t1; t0 += kScanTok) {
-        const int T = min(kScanTok, it.t1 - t0);
-        __syncthreads();
-        for (int i = tid; i < T * P; i += kThreads)
-            s_x[i] = to_f32(x[(static_cast<size_t>(t0 + i / P) * H + h) * P + i % P]);
-        for (int i = tid; i < T * N; i += kThreads) {
-            const size_t at = (static_cast<size_t>(t0 + i / N) * G + g) * N + i % N;
-            s_B[i] = to_f32(B[at]);
-            if (OUT) s_C[i] = to_f32(C[at]);
+    // tokens t0 .. into buffer `to`, zeros past the item's end (a step of
+    // zero keeps the state): one token per 16 threads
+    auto stage = [&](int t0, float* to) {
+        const int s = tid >> 4, l = tid & 15, t = t0 + s;
+        const bool in = t < it.t1;
+        if (l == 0) {
+            const float d = in ? a.dt[static_cast<size_t>(t) * H + h] : 0.f;
+            to[s] = d;
+            to[kScanTok + s] = in ? expf(d * Ah) : 1.f;
         }
-        if (tid < T) s_dt[tid] = a.dt[static_cast<size_t>(t0 + tid) * H + h];
-        __syncthreads();
-        for (int t = 0; t < T; ++t) {
-            const float d = s_dt[t], dec = expf(d * Ah);
-            dtsum += d;
-            const float4 b4 = *reinterpret_cast<const float4*>(s_B + t * N + col);
-            float4 c4 = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (OUT) c4 = *reinterpret_cast<const float4*>(s_C + t * N + col);
+        float* sx = to + 2 * kScanTok + s * xs;
+        float* sB = to + kScanTok * (2 + xs) + s * N;
+        float* sC = sB + kScanTok * N;
+        const TIn* px = x + (static_cast<size_t>(t) * H + h) * P;
+        for (int i = l; i < P; i += 16) sx[i] = in ? to_f32(px[i]) : 0.f;
+        const size_t at = (static_cast<size_t>(t) * G + g) * N;
+        for (int i = l; i < N; i += 16) {
+            sB[i] = in ? to_f32(B[at + i]) : 0.f;
+            if (OUT) sC[i] = in ? to_f32(C[at + i]) : 0.f;
+        }
+    };
+    float dtsum = 0.f;
+    stage(it.t0, sm);
+    int cur = 0;
+    for (int t0 = it.t0; t0 < it.t1; t0 += kScanTok, cur ^= 1) {
+        const int T = min(kScanTok, it.t1 - t0);
+        __syncthreads();  // the tokens are in place; the outputs before have left
+        if (t0 + kScanTok < it.t1) stage(t0 + kScanTok, sm + (cur ^ 1) * buf);
+        const float* s_d = sm + cur * buf;
+        const float* s_x = s_d + 2 * kScanTok;
+        const float* s_B = s_d + kScanTok * (2 + xs);
+        const float* s_C = s_B + kScanTok * N;
+#pragma unroll 1
+        for (int t4 = 0; t4 < T; t4 += 4) {
+            // four tokens: the state's recurrence, then the sums over its rows side by side
+            float part[4][PASS];
 #pragma unroll
-            for (int k = 0; k < PASS; ++k) {
-                const int p = row0 + k * step;
-                const float xp = p < P ? s_x[t * P + p] : 0.f, w = d * xp;
-                st[k].x = fmaf(dec, st[k].x, w * b4.x);
-                st[k].y = fmaf(dec, st[k].y, w * b4.y);
-                st[k].z = fmaf(dec, st[k].z, w * b4.z);
-                st[k].w = fmaf(dec, st[k].w, w * b4.w);
-                if (OUT) {
-                    const float v = group_sum(dot4(st[k], c4), lpr);
-                    if (p < P && (tid & (lpr - 1)) == 0) s_y[t * P + p] = fmaf(Dh, xp, v);
+            for (int j = 0; j < 4; ++j) {
+                const int t = t4 + j;
+                const float d = s_d[t], dec = s_d[kScanTok + t];
+                dtsum += d;
+                const float4 b4 = *reinterpret_cast<const float4*>(s_B + t * N + col);
+                const float4 c4 = OUT ? *reinterpret_cast<const float4*>(s_C + t * N + col) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int k = 0; k < PASS; ++k) {
+                    const int p = row0 + k * step;
+                    const float w = p < P ? d * s_x[t * xs + p] : 0.f;
+                    st[k].x = fmaf(dec, st[k].x, w * b4.x);
+                    st[k].y = fmaf(dec, st[k].y, w * b4.y);
+                    st[k].z = fmaf(dec, st[k].z, w * b4.z);
+                    st[k].w = fmaf(dec, st[k].w, w * b4.w);
+                    part[j][k] = OUT ? dot4(st[k], c4) : 0.f;
                 }
+            }
+            if (OUT) {
+#pragma unroll
+                for (int off = 16; off >= 1; off >>= 1)
+                    if (off < lpr) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+#pragma unroll
+                            for (int k = 0; k < PASS; ++k)
+                                part[j][k] += __shfl_xor_sync(0xffffffffu, part[j][k], off);
+                    }
+                if ((tid & (lpr - 1)) == 0)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+#pragma unroll
+                        for (int k = 0; k < PASS; ++k) {
+                            const int p = row0 + k * step;
+                            if (p < P) s_y[(t4 + j) * P + p] = fmaf(Dh, s_x[(t4 + j) * xs + p], part[j][k]);
+                        }
             }
         }
         if (OUT) {
@@ -1023,31 +1064,73 @@ cudaError_t launch_umma(const ScanArgs& a, int items, cudaStream_t st) {
 template <typename TIn, bool OUT>
 cudaError_t launch_pass(const ScanArgs& a, int items, cudaStream_t st) {
     if (scan_umma_shape(a.s, sizeof(TIn) == 2)) return launch_umma<OUT>(a, items, st);
-    const size_t smem = 4u * kScanTok * (2 * static_cast<size_t>(a.s.P) + 2 * static_cast<size_t>(a.s.N));
+    const size_t xs = (a.s.P + 3) & ~3;
+    const size_t smem = 4u * kScanTok * (2 * (2 + xs + 2 * static_cast<size_t>(a.s.N)) + a.s.P);
     const int passes = (a.s.P * a.s.lpr + kThreads - 1) / kThreads;
     const dim3 grid(static_cast<unsigned>(items) * static_cast<unsigned>(a.s.H));
-    if (passes <= 1)
-        k_scan<TIn, 1, OUT><<<grid, kThreads, smem, st>>>(a);
-    else if (passes <= 4)
-        k_scan<TIn, 4, OUT><<<grid, kThreads, smem, st>>>(a);
-    else if (passes <= 8)
-        k_scan<TIn, 8, OUT><<<grid, kThreads, smem, st>>>(a);
-    else
-        k_scan<TIn, 16, OUT><<<grid, kThreads, smem, st>>>(a);
-    return cudaGetLastError();
+    auto go = [&](auto kernel) {
+        if (smem > 48 * 1024) {
+            const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+            if (e != cudaSuccess) return e;
+        }
+        kernel<<<grid, kThreads, smem, st>>>(a);
+        return cudaGetLastError();
+    };
+    if (passes <= 1) return go(k_scan<TIn, 1, OUT>);
+    if (passes <= 2) return go(k_scan<TIn, 2, OUT>);
+    if (passes <= 4) return go(k_scan<TIn, 4, OUT>);
+    if (passes <= 8) return go(k_scan<TIn, 8, OUT>);
+    return go(k_scan<TIn, 16, OUT>);
 }
 
 }  // namespace
 
+// Whole requests or segments, and which: the least of the times that a simple
+// model of the two kernels gives. A CTA takes `alone` per step while it has an
+// SM to itself and `shared` while it shares one (us per 128 tokens; measured
+// on B200 at head_dim 64, d_state 128) and 5 us to start and end, the pass over
+// the segments' states less; two more launches cost 15 us and the join its
+// bytes. 148 SMs: the
+// workspace must not depend on the device that asks. Measured against whole
+// requests: one prompt of 8192 tokens, 64 heads, 336 -> 186 us in 4 segments;
+// 16 prompts of up to 1501 tokens, 64 heads, 118 us whole and 149 us at best
+// in segments.
 int scan_segment_len(const Shape& s, int in_bf16, int total, int max_seqlen) {
-    (void)in_bf16;
-    // CTAs that fill the GPU; whole requests when there are that many, or
-    // when the longest is short next to the rest of the work
-    const long long fill = 4 * 148;
-    const long long share = static_cast<long long>(total) * s.H / fill;  // tokens per CTA, evenly cut
-    if (max_seqlen <= 256 || max_seqlen <= 2 * share) return 0;
-    const long long len = share < 128 ? 128 : (share + 127) / 128 * 128;
-    if ((total / len + s.batch) * s.H * ((s.P + 63) / 64) > 0x7fffffffLL) return 0;  // one CTA per slot and head
+    struct Cost {
+        int per_sm, tok;      // CTAs that share an SM; tokens per step
+        double alone, shared, state_alone, state_shared;
+    };
+    const bool umma = scan_umma_shape(s, in_bf16);
+    const Cost c = umma ? Cost{2, 128, 5.2, 7.7, 2.6, 3.8} : Cost{4, 128, 20, 40, 14, 28};
+    const double heads = static_cast<double>(s.H) * (umma ? (s.P + 63) / 64 : 1);
+    const long long steps = (static_cast<long long>(max_seqlen) + c.tok - 1) / c.tok;
+    auto rounds = [&](double ctas, double alone, double shared) {  // of CTAs that run at once, in us per step
+        if (ctas <= 148) return alone;
+        const double fit = 148.0 * c.per_sm;
+        return shared * static_cast<double>(static_cast<long long>((ctas + fit - 1) / fit));
+    };
+    const double ctas = heads * s.batch;
+    const double even = heads * (total + 0.5 * c.tok * s.batch) / c.tok / (148.0 * c.per_sm) * c.shared;
+    double best = steps * (ctas <= 148 ? c.alone : c.shared);
+    if (even > best) best = even;
+    best *= 0.95;
+    long long len = 0;
+    for (long long n = 2, before = 0; n <= 64 && n <= steps; ++n) {
+        const long long each = (steps + n - 1) / n, tokens = each * c.tok;
+        if (each == before) continue;
+        before = each;
+        const double segs = static_cast<double>((total + tokens - 1) / tokens) + 0.5 * (s.batch - 1);
+        const double inner = segs - s.batch > 0 ? segs - s.batch : 0;
+        const double join = s.H * (segs + s.batch) * s.P * s.N * 12 / 5e6;  // us
+        const double t = each * (rounds(heads * segs, c.alone, c.shared) +
+                                 (inner > 0 ? rounds(heads * inner, c.state_alone, c.state_shared) : 0)) +
+                         rounds(heads * segs, 5, 5) + (inner > 0 ? rounds(heads * inner, 5, 5) : 0) + 15 + join;
+        // one CTA per slot and head
+        if (t < best && (total / tokens + s.batch) * static_cast<long long>(heads) <= 0x7fffffffLL) {
+            best = t;
+            len = tokens;
+        }
+    }
     return static_cast<int>(len);
 }
 
