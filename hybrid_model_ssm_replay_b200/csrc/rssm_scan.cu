@@ -105,15 +105,53 @@ __device__ __forceinline__ float* slot_dtsum(const ScanArgs& a, int slot, int h)
     return a.ws + static_cast<size_t>(scan_slots(a)) * a.s.H * a.s.P * a.s.N + static_cast<size_t>(slot) * a.s.H + h;
 }
 
+// Two fp32 lanes in one instruction.
+#define RSSM_F32X2(name, op)                                                       \
+    __device__ __forceinline__ float2 name(float2 a, float2 b) {                   \
+        float2 d;                                                                  \
+        asm("{\n\t.reg .b64 ra, rb, rd;\n\t"                                       \
+            "mov.b64 ra, {%2, %3};\n\t"                                            \
+            "mov.b64 rb, {%4, %5};\n\t" op                                         \
+            " rd, ra, rb;\n\t"                                                     \
+            "mov.b64 {%0, %1}, rd;\n\t}"                                           \
+            : "=f"(d.x), "=f"(d.y)                                                 \
+            : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));                             \
+        return d;                                                                  \
+    }
+RSSM_F32X2(add2, "add.rn.f32x2")
+RSSM_F32X2(sub2, "sub.rn.f32x2")
+RSSM_F32X2(mul2, "mul.rn.f32x2")
+#undef RSSM_F32X2
+
 // ---------------------------------------------------------------------------
 // k_scan: the recurrence token by token, for every shape and both input
 // types. One CTA per (item, head); the state stays in registers, lane group
 // of N / 4 lanes per state row, 4 columns per lane, PASS rows per thread;
 // tokens are staged 16 at a time in shared memory as fp32, the next ones
-// while these are worked on, and worked on 4 at a time: bound by the latency
-// of the row sums' shuffles otherwise. @KSCAN@
+// while these are worked on, and worked on 4 at a time, with the sums of
+// their rows shared out over the lanes (31 shuffles for 32 sums). Bound by
+// instruction issue. B200, fp32, 32 prompts of 300 tokens, 64 heads of
+// 64 x 128: 2.07 ms with a shuffle per row and token and scalar FMAs, 1.22 ms
+// as it is.
 // ---------------------------------------------------------------------------
 constexpr int kScanTok = 16;
+
+// One step of a sum over lanes of several values side by side: lanes `off`
+// apart share out the V values, each keeps the sums of half of them (the
+// lane with the bit `off` the second half). V = 1: both keep it.
+template <int V, int M>
+__device__ __forceinline__ void share_sums(float (&v)[M], int off) {
+    if constexpr (V == 1) {
+        v[0] += __shfl_xor_sync(0xffffffffu, v[0], off);
+    } else {
+        const bool up = threadIdx.x & off;
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) {
+            const float send = up ? v[i] : v[i + V / 2], keep = up ? v[i + V / 2] : v[i];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, off);
+        }
+    }
+}
 
 template <typename TIn, int PASS, bool OUT>
 __global__ void __launch_bounds__(kThreads) k_scan(const ScanArgs a) {
@@ -128,12 +166,14 @@ __global__ void __launch_bounds__(kThreads) k_scan(const ScanArgs a) {
     float* s_y = sm + 2 * buf;  // [kScanTok][P]
     const int col = 4 * (tid & (lpr - 1)), row0 = tid / lpr, step = kThreads / lpr;
     const float* init = it.slot < 0 ? head_state(a, it.b, h) : slot_state(a, it.slot, h);
-    float4 st[PASS];
+    float2 st[PASS][2];
 #pragma unroll
     for (int k = 0; k < PASS; ++k) {
         const int p = row0 + k * step;
-        st[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (OUT && p < P) st[k] = *reinterpret_cast<const float4*>(init + static_cast<size_t>(p) * N + col);
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (OUT && p < P) v = *reinterpret_cast<const float4*>(init + static_cast<size_t>(p) * N + col);
+        st[k][0] = make_float2(v.x, v.y);
+        st[k][1] = make_float2(v.z, v.w);
     }
     const float Ah = a.A[h], Dh = OUT ? a.D[h] : 0.f;
     const TIn* x = static_cast<const TIn*>(a.x);
@@ -173,44 +213,71 @@ __global__ void __launch_bounds__(kThreads) k_scan(const ScanArgs a) {
         const float* s_C = s_B + kScanTok * N;
 #pragma unroll 1
         for (int t4 = 0; t4 < T; t4 += 4) {
-            // four tokens: the state's recurrence, then the sums over its rows side by side
-            float part[4][PASS];
+            // four tokens: the state's recurrence, then the sums over its rows side
+            // by side (value j PASS + k: token j, row k), shared out over the lanes
+            constexpr int V = 4 * PASS;
+            float part[V];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int t = t4 + j;
                 const float d = s_d[t], dec = s_d[kScanTok + t];
                 dtsum += d;
+                const float2 dec2 = make_float2(dec, dec);
                 const float4 b4 = *reinterpret_cast<const float4*>(s_B + t * N + col);
-                const float4 c4 = OUT ? *reinterpret_cast<const float4*>(s_C + t * N + col) : make_float4(0.f, 0.f, 0.f, 0.f);
+                const float2 b0 = make_float2(b4.x, b4.y), b1 = make_float2(b4.z, b4.w);
+                float2 c0, c1;
+                if (OUT) {
+                    const float4 c4 = *reinterpret_cast<const float4*>(s_C + t * N + col);
+                    c0 = make_float2(c4.x, c4.y);
+                    c1 = make_float2(c4.z, c4.w);
+                }
 #pragma unroll
                 for (int k = 0; k < PASS; ++k) {
                     const int p = row0 + k * step;
                     const float w = p < P ? d * s_x[t * xs + p] : 0.f;
-                    st[k].x = fmaf(dec, st[k].x, w * b4.x);
-                    st[k].y = fmaf(dec, st[k].y, w * b4.y);
-                    st[k].z = fmaf(dec, st[k].z, w * b4.z);
-                    st[k].w = fmaf(dec, st[k].w, w * b4.w);
-                    part[j][k] = OUT ? dot4(st[k], c4) : 0.f;
+                    const float2 w2 = make_float2(w, w);
+                    st[k][0] = fma2(dec2, st[k][0], mul2(w2, b0));
+                    st[k][1] = fma2(dec2, st[k][1], mul2(w2, b1));
+                    if (OUT) {
+                        const float2 y2 = fma2(st[k][0], c0, mul2(st[k][1], c1));
+                        part[j * PASS + k] = y2.x + y2.y;
+                    }
                 }
             }
             if (OUT) {
-#pragma unroll
-                for (int off = 16; off >= 1; off >>= 1)
-                    if (off < lpr) {
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-#pragma unroll
-                            for (int k = 0; k < PASS; ++k)
-                                part[j][k] += __shfl_xor_sync(0xffffffffu, part[j][k], off);
+                auto put = [&](int n, int steps) {  // the n values of this lane after `steps` steps
+                    int first = 0;
+                    bool mine = true;
+                    for (int i = 0, half = V / 2; i < steps; ++i, half /= 2) {
+                        if (half) first += tid & (1 << i) ? half : 0;
+                        else if (tid & (1 << i)) mine = false;
                     }
-                if ((tid & (lpr - 1)) == 0)
+                    if (!mine) return;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-#pragma unroll
-                        for (int k = 0; k < PASS; ++k) {
-                            const int p = row0 + k * step;
-                            if (p < P) s_y[(t4 + j) * P + p] = fmaf(Dh, s_x[(t4 + j) * xs + p], part[j][k]);
+                    for (int i = 0; i < V / 4; ++i) {
+                        const int j = (first + i) / PASS, p = row0 + (first + i) % PASS * step;
+                        if (i < n && p < P) s_y[(t4 + j) * P + p] = fmaf(Dh, s_x[(t4 + j) * xs + p], part[i]);
+                    }
+                };
+                share_sums<V>(part, 1);
+                share_sums<V / 2>(part, 2);
+                if (lpr == 4) {
+                    put(V / 4, 2);
+                } else {
+                    share_sums<V / 4>(part, 4);
+                    constexpr int V3 = V / 8 ? V / 8 : 1, V4 = V / 16 ? V / 16 : 1, V5 = V / 32 ? V / 32 : 1;
+                    if (lpr == 8) {
+                        put(V3, 3);
+                    } else {
+                        share_sums<V3>(part, 8);
+                        if (lpr == 16) {
+                            put(V4, 4);
+                        } else {
+                            share_sums<V4>(part, 16);
+                            put(V5, 5);
                         }
+                    }
+                }
             }
         }
         if (OUT) {
@@ -224,7 +291,9 @@ __global__ void __launch_bounds__(kThreads) k_scan(const ScanArgs a) {
 #pragma unroll
     for (int k = 0; k < PASS; ++k) {
         const int p = row0 + k * step;
-        if (p < P) *reinterpret_cast<float4*>(out + static_cast<size_t>(p) * N + col) = st[k];
+        if (p < P)
+            *reinterpret_cast<float4*>(out + static_cast<size_t>(p) * N + col) =
+                make_float4(st[k][0].x, st[k][0].y, st[k][1].x, st[k][1].y);
     }
     if (!OUT && tid == 0) *slot_dtsum(a, it.slot, h) = dtsum;
 }
@@ -373,24 +442,6 @@ __device__ __forceinline__ uint32_t pack_bf16(float2 v) {
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(v.y), "f"(v.x));
     return d;
 }
-
-// Two fp32 lanes in one instruction.
-#define RSSM_F32X2(name, op)                                                       \
-    __device__ __forceinline__ float2 name(float2 a, float2 b) {                   \
-        float2 d;                                                                  \
-        asm("{\n\t.reg .b64 ra, rb, rd;\n\t"                                       \
-            "mov.b64 ra, {%2, %3};\n\t"                                            \
-            "mov.b64 rb, {%4, %5};\n\t" op                                         \
-            " rd, ra, rb;\n\t"                                                     \
-            "mov.b64 {%0, %1}, rd;\n\t}"                                           \
-            : "=f"(d.x), "=f"(d.y)                                                 \
-            : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));                             \
-        return d;                                                                  \
-    }
-RSSM_F32X2(add2, "add.rn.f32x2")
-RSSM_F32X2(sub2, "sub.rn.f32x2")
-RSSM_F32X2(mul2, "mul.rn.f32x2")
-#undef RSSM_F32X2
 
 // A pair of bf16 with zeros in the place of NaN and infinities.
 __device__ __forceinline__ uint32_t finite2(uint32_t w) {
@@ -1101,7 +1152,7 @@ int scan_segment_len(const Shape& s, int in_bf16, int total, int max_seqlen) {
         double alone, shared, state_alone, state_shared;
     };
     const bool umma = scan_umma_shape(s, in_bf16);
-    const Cost c = umma ? Cost{2, 128, 5.2, 7.7, 2.6, 3.8} : Cost{4, 128, 20, 40, 14, 28};
+    const Cost c = umma ? Cost{2, 128, 5.2, 7.7, 2.6, 3.8} : Cost{4, 128, 45, 150, 27, 80};
     const double heads = static_cast<double>(s.H) * (umma ? (s.P + 63) / 64 : 1);
     const long long steps = (static_cast<long long>(max_seqlen) + c.tok - 1) / c.tok;
     auto rounds = [&](double ctas, double alone, double shared) {  // of CTAs that run at once, in us per step
