@@ -339,7 +339,7 @@ __global__ void __launch_bounds__(kThreads) k_scan(const ScanArgs a) {
 // ---------------------------------------------------------------------------
 constexpr int kSuTok = 128;                    // tokens per block
 constexpr int kSuThreads = 256;
-constexpr int kSuIssuer = 4;                   // two warps with none of M's lower triangle: of the products
+constexpr int kSuIssuer = 4;                   // two warps with less of M's lower triangle: of the products
 constexpr int kSuStorer = 5;                   // and of the second half of Y
 constexpr uint32_t kSuBlk = kSuTok * 128u;     // 128 rows of 128 bytes, swizzled: 16 KB
 constexpr uint32_t kSuB = 0;                   // B rows, two 64-column blocks
@@ -674,20 +674,21 @@ __global__ void __launch_bounds__(kSuThreads, 2)
             const float4 mine = s_sum[q];
             const float pre32 = pre + ((oct > 0 ? mine.x : 0.f) + (oct > 1 ? mine.y : 0.f) + (oct > 2 ? mine.z : 0.f));
             const float before = (q > 0 ? sums.x : 0.f) + (q > 1 ? sums.y : 0.f) + (q > 2 ? sums.z : 0.f);
-            // M over S, 32-blocks 2 half and 2 half + 1 of its columns, 16 at a
-            // time: hi and mid parts in the columns read, lo in its own
-            auto put_m = [&](int J, int k, const float2 (&m)[8]) {
+            // M over S, columns 16 half .. + 15 of each of its 32-blocks: hi and mid
+            // parts in the columns read, lo in its own
+            auto put_m = [&](int J, const float2 (&m)[8]) {
                 uint32_t hi[8], mid[8], lo[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) split3(m[i], hi[i], mid[i], lo[i]);
-                su_st8(tml + kTmS + 32 * J + 16 * k, hi);
-                su_st8(tml + kTmS + 32 * J + 16 * k + 8, mid);
-                su_st8(tml + kTmLo + 16 * J + 8 * k, lo);
+                const uint32_t at = 32 * J + 16 * half;
+                su_st8(tml + kTmS + at, hi);
+                su_st8(tml + kTmS + at + 8, mid);
+                su_st8(tml + kTmLo + at / 2, lo);
             };
-            // column factors of columns 16 k .. of 32-block J; f0, f1: decay from the
-            // end of their two groups of 8 to this token
-            auto factors = [&](int J, int k, float f0, float f1, float2 (&m)[8]) {
-                const float4* c4 = reinterpret_cast<const float4*>(s_col + 32 * J + 16 * k);
+            // their column factors in 32-block J; f0, f1: decay from the end of their
+            // two groups of 8 to this token
+            auto factors = [&](int J, float f0, float f1, float2 (&m)[8]) {
+                const float4* c4 = reinterpret_cast<const float4*>(s_col + 32 * J + 16 * half);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float4 c = c4[i];
@@ -696,83 +697,63 @@ __global__ void __launch_bounds__(kSuThreads, 2)
                     m[2 * i + 1] = mul2(f2, make_float2(c.z, c.w));
                 }
             };
-            if ((q >> 1) == half) {  // the block on the diagonal
-                // the same 8 tokens' factors, from the running sum: A2 times the dt
-                // sum from s + 1 to t; zero for later tokens
-                uint32_t own[8];
-                const int l7 = lane & 7;
-                float run = 0.f, dnx = 0.f;
+            // the block on the diagonal: factors from the running sum, A2 times the
+            // dt sum from s + 1 to t, downwards from the last column; zero for later
+            // tokens (whose S may be NaN)
+            float f[16];
+            {
+                float run = half || oct < 2 ? 0.f : A2 * (pre + (oct > 2 ? mine.z : 0.f));
+                float dnx = 0.f;
 #pragma unroll
-                for (int j = 7; j >= 0; --j) {
-                    const float ds = __shfl_sync(0xffffffffu, d, j, 8);
-                    run = fmaf(A2, l7 > j ? dnx : 0.f, run);
+                for (int j = 15; j >= 0; --j) {
+                    const float ds = __shfl_sync(0xffffffffu, d, 16 * half + j);
+                    run = fmaf(A2, lane > 16 * half + j ? dnx : 0.f, run);
                     dnx = ds;
-                    own[j] = __float_as_uint(ds * su_exp2(run)) & static_cast<uint32_t>(~((l7 - j) >> 31));
+                    f[j] = ds * su_exp2(run);
                 }
-                if (!su_wait(bar_s, par)) timed_out = true;
-                su_fence_after();
-#pragma unroll 1
-                for (int k = 0; k < 2; ++k) {
-                    uint32_t v[16];
-                    su_ld16(tml + kTmS + 32 * q + 16 * k, v);
-                    const float z2 = oct > 2 ? mine.z : 0.f, y2 = (oct > 1 ? mine.y : 0.f) + z2;
-                    float2 m[8];
-                    factors(q, k, su_exp2(A2 * (pre + (k ? 0.f : y2))), su_exp2(A2 * (pre + (k ? 0.f : z2))), m);
-                    su_wait_ld();
-                    // by masks, not branches: every lane goes another way (S and the
-                    // factor of a later token may be NaN)
+            }
+            if (!su_wait(bar_s, par)) timed_out = true;
+            su_fence_after();
+            {
+                uint32_t v[16];
+                su_ld16(tml + kTmS + 32 * q + 16 * half, v);
+                su_wait_ld();
+                float2 m[8];
 #pragma unroll
-                    for (int o = 0; o < 2; ++o) {
-                        const uint32_t eq = oct == 2 * k + o ? ~0u : 0u, gt = oct > 2 * k + o ? ~0u : 0u;
-                        const uint32_t De = __float_as_uint(Dh) & eq;
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const int i = 4 * o + j / 2;
-                            const uint32_t w = (own[j] & eq) | (__float_as_uint(j & 1 ? m[i].y : m[i].x) & gt);
-                            const uint32_t seen = gt | (eq & static_cast<uint32_t>(~((l7 - j) >> 31)));
-                            const uint32_t dx = l7 == j ? De : 0u;  // D x_t
-                            const float e = fmaf(__uint_as_float(v[8 * o + j] & seen), __uint_as_float(w),
-                                                 __uint_as_float(dx));
-                            if (j & 1)
-                                m[i].y = e;
-                            else
-                                m[i].x = e;
-                        }
-                    }
-                    put_m(q, k, m);
+                for (int j = 0; j < 16; ++j) {
+                    const int c = lane - (16 * half + j);
+                    float e = fmaf(__uint_as_float(v[j]), f[j], c == 0 ? Dh : 0.f);  // D x_t
+                    e = c >= 0 ? e : 0.f;
+                    if (j & 1)
+                        m[j / 2].y = e;
+                    else
+                        m[j / 2].x = e;
                 }
-            } else {
-                if (!su_wait(bar_s, par)) timed_out = true;
-                su_fence_after();
+                put_m(q, m);
             }
 #pragma unroll 1
-            for (int J = 2 * half; J < 2 * half + 2; ++J) {
+            for (int J = 0; J < 4; ++J) {
                 if (J == q) continue;
                 if (J > q) {  // nothing but later tokens
                     const uint32_t zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        su_st8(tml + kTmS + 32 * J + 16 * k, zero);
-                        su_st8(tml + kTmS + 32 * J + 16 * k + 8, zero);
-                        su_st8(tml + kTmLo + 16 * J + 8 * k, zero);
-                    }
+                    const uint32_t at = 32 * J + 16 * half;
+                    su_st8(tml + kTmS + at, zero);
+                    su_st8(tml + kTmS + at + 8, zero);
+                    su_st8(tml + kTmLo + at / 2, zero);
                     continue;
                 }
+                uint32_t v[16];
+                su_ld16(tml + kTmS + 32 * J + 16 * half, v);
                 const float4 o = s_sum[J];
                 const float to = pre32 + ((J < 1 && q > 1 ? sums.y : 0.f) + (J < 2 && q > 2 ? sums.z : 0.f));
-#pragma unroll 1
-                for (int k = 0; k < 2; ++k) {
-                    uint32_t v[16];
-                    su_ld16(tml + kTmS + 32 * J + 16 * k, v);
-                    float2 m[8];
-                    factors(J, k, su_exp2(A2 * (to + (k ? o.w : o.y + o.z + o.w))),
-                            su_exp2(A2 * (to + (k ? 0.f : o.z + o.w))), m);
-                    su_wait_ld();
+                float2 m[8];
+                factors(J, su_exp2(A2 * (to + (half ? o.w : o.y + o.z + o.w))),
+                        su_exp2(A2 * (to + (half ? 0.f : o.z + o.w))), m);
+                su_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        m[i] = mul2(m[i], make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])));
-                    put_m(J, k, m);
-                }
+                for (int i = 0; i < 8; ++i)
+                    m[i] = mul2(m[i], make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])));
+                put_m(J, m);
             }
             // the state's share of the outputs, scaled in place; Y is added to it
             const float fac = su_exp2(A2 * (before + pre32));
@@ -799,13 +780,12 @@ __global__ void __launch_bounds__(kSuThreads, 2)
             su_wait_st();
         }
         // w x in three parts, 32 passes over 4 token rows, a 16-byte chunk per
-        // thread and pass. With M to build, a warp has 0, 1 or 2 of its 32 x 32
-        // blocks, the diagonal ones dearer: the passes even that out among the
-        // warps, and among the four warps of each q, which share a scheduler.
+        // thread and pass. With M to build, a warp has the more of it the larger
+        // q, and the issuer waits on the products: the passes even that out.
         const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
         __nv_bfloat162 z = zero;  // NaN when x has a NaN or infinity
-        constexpr uint64_t kFirst = OUT ? 0x1E1A110E0B080500ull : 0x1C1814100C080400ull;  // byte w: warp w's first pass
-        constexpr uint32_t kPasses = OUT ? 0x24933335u : 0x44444444u;                      // digit w: how many
+        constexpr uint64_t kFirst = OUT ? 0x1E1A1414120E0800ull : 0x1C1814100C080400ull;  // byte w: warp w's first pass
+        constexpr uint32_t kPasses = OUT ? 0x24602468u : 0x44444444u;                      // digit w: how many
         const int first = static_cast<int>((kFirst >> (8 * warp)) & 31), passes = (kPasses >> (4 * warp)) & 15;
         if (!su_wait(bar_x, par)) timed_out = true;
 #pragma unroll 1
