@@ -1134,7 +1134,8 @@ int scan_segment_len(const Shape& s, int in_bf16, int total, int max_seqlen) {
     const bool umma = scan_umma_shape(s, in_bf16);
     const Cost c = umma ? Cost{2, 128, 5.2, 7.7, 2.6, 3.8} : Cost{4, 128, 45, 150, 27, 80};
     const double heads = static_cast<double>(s.H) * (umma ? (s.P + 63) / 64 : 1);
-    const long long steps = (static_cast<long long>(max_seqlen) + c.tok - 1) / c.tok;
+    const long long longest = max_seqlen < total ? max_seqlen : total;
+    const long long steps = (longest + c.tok - 1) / c.tok;
     auto rounds = [&](double ctas, double alone, double shared) {  // of CTAs that run at once, in us per step
         if (ctas <= 148) return alone;
         const double fit = 148.0 * c.per_sm;

@@ -560,22 +560,25 @@ __global__ void __launch_bounds__(512) k_add_norm_rows(const AddNormArgs a, cons
     }
 }
 
-// Any other width: one CTA per row, element by element, 16 elements per
-// thread in registers and the rest of a wide row read again.
-constexpr int kAddKeep = 16;
+// Any other width: `warps` warps per row, element by element, kAddKeep elements
+// per lane in registers and the rest of a wide row read again. B200, 5003 rows
+// of 2561, fp32 stream (154 MB): @ADDANY@.
+constexpr int kAddKeep = 12;
 template <typename TU>
-__global__ void __launch_bounds__(kNormThreads) k_add_norm_any(const AddNormArgs a) {
+__global__ void __launch_bounds__(kNormThreads) k_add_norm_any(const AddNormArgs a, const int warps) {
     __shared__ float red[kNormThreads / 32];
-    constexpr int kW = kNormThreads / 32;
-    const size_t r0 = static_cast<size_t>(blockIdx.x) * a.dim;
-    const int dim = a.dim;
+    const int l = threadIdx.x & (32 * warps - 1), step = 32 * warps;
+    const long long row = static_cast<long long>(blockIdx.x) * (kNormThreads / 32 / warps) + (threadIdx.x >> 5) / warps;
+    const int dim = row < a.rows ? a.dim : 0;  // (a team without a row takes part in the sums)
+    const size_t r0 = dim ? static_cast<size_t>(row) * a.dim : 0;
+    const float inv_n = 1.0f / static_cast<float>(a.dim);
     const TU* u = static_cast<const TU*>(a.u) + r0;
     TU* uo = a.u_out ? static_cast<TU*>(a.u_out) + r0 : nullptr;
     const __nv_bfloat16* v = a.v ? a.v + r0 : nullptr;
     float ku[kAddKeep], kv[kAddKeep];
 #pragma unroll
     for (int k = 0; k < kAddKeep; ++k) {
-        const int i = threadIdx.x + k * kNormThreads;
+        const int i = l + k * step;
         ku[k] = i < dim ? to_f(u[i]) : 0.f;
         kv[k] = v && i < dim ? bf(v[i]) : 0.f;
     }
@@ -584,8 +587,8 @@ __global__ void __launch_bounds__(kNormThreads) k_add_norm_any(const AddNormArgs
         float ss = 0.f;
 #pragma unroll
         for (int k = 0; k < kAddKeep; ++k) ss = fmaf(kv[k], kv[k], ss);
-        for (int i = threadIdx.x + kAddKeep * kNormThreads; i < dim; i += kNormThreads) ss = fmaf(bf(v[i]), bf(v[i]), ss);
-        inv = rsqrtf(row_sum(ss, kW, red) / static_cast<float>(dim) + a.eps);
+        for (int i = l + kAddKeep * step; i < dim; i += step) ss = fmaf(bf(v[i]), bf(v[i]), ss);
+        inv = rsqrtf(row_sum(ss, warps, red) * inv_n + a.eps);
     }
     auto stream = [&](int i, float t, float f) {  // u' as it is kept
         if (v) {
@@ -600,7 +603,7 @@ __global__ void __launch_bounds__(kNormThreads) k_add_norm_any(const AddNormArgs
     float ss = 0.f;
 #pragma unroll
     for (int k = 0; k < kAddKeep; ++k) {
-        const int i = threadIdx.x + k * kNormThreads;
+        const int i = l + k * step;
         if (i < dim) {
             const TU t = stream(i, ku[k], kv[k]);
             if (uo) uo[i] = t;
@@ -608,19 +611,19 @@ __global__ void __launch_bounds__(kNormThreads) k_add_norm_any(const AddNormArgs
         }
         ss = fmaf(ku[k], ku[k], ss);
     }
-    for (int i = threadIdx.x + kAddKeep * kNormThreads; i < dim; i += kNormThreads) {
+    for (int i = l + kAddKeep * step; i < dim; i += step) {
         const TU t = stream(i, to_f(u[i]), v ? bf(v[i]) : 0.f);
         if (a.out) ss = fmaf(to_f(t), to_f(t), ss);
         if (uo && !a.out) uo[i] = t;
     }
     if (!a.out) return;
-    const float pre = rsqrtf(row_sum(ss, kW, red) / static_cast<float>(dim) + a.eps);
+    const float pre = rsqrtf(row_sum(ss, warps, red) * inv_n + a.eps);
 #pragma unroll
     for (int k = 0; k < kAddKeep; ++k) {
-        const int i = threadIdx.x + k * kNormThreads;
+        const int i = l + k * step;
         if (i < dim) a.out[r0 + i] = __float2bfloat16_rn(ku[k] * pre * a.pre_w[i]);
     }
-    for (int i = threadIdx.x + kAddKeep * kNormThreads; i < dim; i += kNormThreads) {
+    for (int i = l + kAddKeep * step; i < dim; i += step) {
         const TU t = stream(i, to_f(u[i]), v ? bf(v[i]) : 0.f);
         if (uo) uo[i] = t;
         a.out[r0 + i] = __float2bfloat16_rn(to_f(t) * pre * a.pre_w[i]);
@@ -773,10 +776,14 @@ rssm_status_t rssm_stage_add_norm(int32_t rows, int32_t dim, int32_t u_dtype, co
             k_add_norm_rows<float><<<grid, threads, 0, st>>>(a, warps);
         else
             k_add_norm_rows<__nv_bfloat16><<<grid, threads, 0, st>>>(a, warps);
-    } else if (u_dtype == RSSM_F32) {
-        k_add_norm_any<float><<<static_cast<unsigned>(rows), kNormThreads, 0, st>>>(a);
     } else {
-        k_add_norm_any<__nv_bfloat16><<<static_cast<unsigned>(rows), kNormThreads, 0, st>>>(a);
+        int warps = 1;  // per row, the elements that lanes keep
+        while (warps < kNormThreads / 32 && 32 * kAddKeep * warps < dim) warps *= 2;
+        const unsigned grid = static_cast<unsigned>((rows - 1) / (kNormThreads / 32 / warps) + 1);
+        if (u_dtype == RSSM_F32)
+            k_add_norm_any<float><<<grid, kNormThreads, 0, st>>>(a, warps);
+        else
+            k_add_norm_any<__nv_bfloat16><<<grid, kNormThreads, 0, st>>>(a, warps);
     }
     return launched();
 }

@@ -143,8 +143,9 @@ def _arg(t, dtype, shape, name, dev):
 
 
 def _stream(stream=None):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ct.c_void_p(s.cuda_stream)
+    if stream is None:  # the current stream's handle, without making a Stream object of it
+        return ct.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
+    return ct.c_void_p(stream.cuda_stream)
 
 
 def make_desc(batch, nheads, head_dim, d_state, ngroups, interval=16, max_draft=0, in_dtype=RSSM_BF16,

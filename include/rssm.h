@@ -289,7 +289,7 @@ RSSM_API rssm_status_t rssm_prefill(const rssm_desc_t *desc, const rssm_state_t 
  * cu_seqlens[b] .. cu_seqlens[b+1]-1 of every per-token array; cu_seqlens is
  * a device int32 [batch+1], not decreasing, within 0..total. A request may
  * have no tokens. Rows of no request (before cu_seqlens[0], from
- * cu_seqlens[batch] on) are neither read nor written. */
+ * cu_seqlens[batch] on) are not written, and what they hold does not matter. */
 
 /* Selective scan of packed prompts with their outputs -- the prefill of a
  * layer whose outputs the next layer needs (the article is silent on it):
@@ -308,7 +308,11 @@ RSSM_API rssm_status_t rssm_prefill(const rssm_desc_t *desc, const rssm_state_t 
  *               alone until it has run; NULL where that is 0
  * A long prompt of few requests is cut into segments that run at once: their
  * states from zero, then the states joined in order, then the outputs from
- * the joined states. Sums and the carried state are fp32.
+ * the joined states. Sums and the carried state are fp32. With bf16 inputs
+ * and head_dim a multiple of 8 the products run on the tensor cores, fp32
+ * factors in bf16 parts: three of the weighted x and of the products of
+ * tokens (errors of 2^-26 of a term), two of the state that an output reads
+ * (2^-18).
  * A NaN or infinity in the inputs of a token reaches that token and later
  * ones of its request (of x: in its head_dim column), none before it.
  * Requires an fp32 state (update_dtype F32, no output copy), else

@@ -194,6 +194,37 @@ def test_scan_bad_values_stay_behind(what, value, dtype):
         near(to_np(st.ckpt[0][keep]), to_np(h0[0][keep]), "the other rows of the state")
 
 
+@pytest.mark.parametrize("shape", [LayerShape(2, 2, 64, 128, 1), LayerShape(2, 2, 40, 64, 1)], ids=["P64N128", "P40N64"])
+@pytest.mark.parametrize("lens", [[300, 40], [1300, 40]], ids=["whole", "segments"])
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+def test_scan_rows_of_others_do_not_matter(shape, lens, dtype):
+    """NaN in every row of the next request and of no request, and in the
+    columns of the other head, changes nothing of a request."""
+    p = Packed(shape, lens, 55, dtype, first=3)
+    st0 = p.run()
+    y0, n = p.y.clone(), lens[0]
+    rows = torch.ones(p.T, dtype=torch.bool, device="cuda")
+    rows[3:3 + n] = False
+    for k in ("x", "B", "C", "dt"):
+        getattr(p, k)[rows] = float("nan")
+    p.x[:, 1] = float("nan")  # the second head
+    st = p.run()
+    assert rssm.rssm_get_error(st) == 0
+    assert torch.equal(p.y[3:3 + n, 0], y0[3:3 + n, 0]) and torch.equal(st.ckpt[0, 0], st0.ckpt[0, 0])
+
+
+def test_scan_loose_bound_on_the_lengths():
+    """max_seqlen only bounds the lengths: any larger one gives the same."""
+    p = Packed(LayerShape(3, 2, 64, 128, 1), [200, 5, 129], 56)
+    p.run()
+    y, n = p.y.clone(), sum(p.lens)
+    for longest in (201, 1 << 20, (1 << 31) - 1):
+        p.y.fill_(float("nan"))
+        st = p.run(longest=longest)
+        assert rssm.rssm_get_error(st) == 0
+        near(to_np(p.y[:n]), to_np(y[:n]), f"max_seqlen {longest}")
+
+
 def test_scan_device_errors_leave_the_request():
     shape = LayerShape(3, 2, 64, 128, 1)
     p = Packed(shape, [20, 30, 25], 61)
