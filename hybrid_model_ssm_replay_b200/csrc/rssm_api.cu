@@ -314,15 +314,15 @@ rssm_status_t rssm_prefill_scan(const rssm_desc_t* d, const rssm_state_t* st, in
     if (total > 0 && (!x || !B || !C || !dt || !A || !D || !y)) return RSSM_ERR_INVALID_ARG;
     if (!aligned16({x, B, C, dt, A, D, y, workspace})) return RSSM_ERR_INVALID_ARG;
     if (total == 0) return RSSM_OK;
-    const size_t need = rssm_prefill_scan_workspace_bytes(d, total, max_seqlen);
-    if (need > 0 && !workspace) return RSSM_ERR_INVALID_ARG;
-    if (workspace_bytes < need) return RSSM_ERR_CAPACITY;
     const int bf16 = d->in_dtype == RSSM_BF16;
     ScanArgs a;
     a.s = shape_of(d);
     a.total = total;
     a.max_seqlen = max_seqlen;
     a.seg_len = max_seqlen > 0 ? scan_segment_len(a.s, bf16, total, max_seqlen) : 0;
+    const size_t need = scan_workspace_bytes(a.s, total, a.seg_len);
+    if (need > 0 && !workspace) return RSSM_ERR_INVALID_ARG;
+    if (workspace_bytes < need) return RSSM_ERR_CAPACITY;
     a.cu = cu_seqlens;
     a.rec = rec_of(d);
     a.record = static_cast<unsigned char*>(st->record);

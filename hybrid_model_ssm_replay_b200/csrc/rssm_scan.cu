@@ -1076,6 +1076,19 @@ bool encode_out(CUtensorMap* m, float* base, int total, int H, int P) {
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Lets a kernel use `bytes` of dynamic shared memory, once per device.
+template <typename K>
+cudaError_t allow_smem(K kernel, size_t bytes, std::atomic<uint64_t>& done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev >= 0 && dev < 64 ? 1ull << dev : 0;
+    if (bit && (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+    return e;
+}
+
 template <bool OUT>
 cudaError_t launch_umma(const ScanArgs& a, int items, cudaStream_t st) {
     const int slices = (a.s.P + 63) / 64;
@@ -1084,8 +1097,8 @@ cudaError_t launch_umma(const ScanArgs& a, int items, cudaStream_t st) {
     if (!encode_rows(&mx, a.x, a.total, xw) || !encode_rows(&mb, a.B, a.total, bw) ||
         !encode_rows(&mc, a.C, a.total, bw) || !encode_out(&my, a.y, a.total, a.s.H, a.s.P))
         return cudaErrorInvalidValue;
-    cudaError_t e = cudaFuncSetAttribute(k_scan_umma<OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(kSuSmem));
+    static std::atomic<uint64_t> allowed{0};
+    const cudaError_t e = allow_smem(k_scan_umma<OUT>, kSuSmem, allowed);
     if (e != cudaSuccess) return e;
     const dim3 grid(static_cast<unsigned>(items) * static_cast<unsigned>(a.s.H) * static_cast<unsigned>(slices));
     k_scan_umma<OUT><<<grid, kSuThreads, kSuSmem, st>>>(a, mx, mb, mc, my, slices);
