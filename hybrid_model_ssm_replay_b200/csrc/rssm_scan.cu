@@ -332,6 +332,20 @@ __global__ void __launch_bounds__(kThreads) k_scan(const ScanArgs a) {
 // two (2^-18) of the state, which the next block reads from fp32 again,
 // give 3e-7.
 //
+// What bounds it. B200, 256 prompts of 512 tokens, 64 heads of 64 x 128
+// (4.87 GB, 0.74 ms at the copy rate): 1.76 ms in bursts, 2.06 ms back to back
+// under the power cap. Per block and head the tensor pipe is busy 2500 of
+// 7200 cycles, the schedulers issue in 49 % of theirs, the shared-memory data
+// pipe is busy 70 % of its (loads and stores half of it, the products'
+// operands the other); each CTA is a chain of load, S, M, Y, U and state, and
+// two CTAs (all that tensor memory and shared memory hold) overlap no more of
+// it. Steps that paid: TMA for the operands, outputs through shared memory and
+// TMA instead of a row per lane (a quarter of the time), M's diagonal blocks
+// without branches, code short enough for the instruction cache, even shares
+// for the warps. Steps that did not: 512 threads at 64 registers (spills go to
+// L2, since shared memory leaves no L1), 512 threads alone on an SM (5 % on
+// few long prompts).
+//
 // x is the one raw operand of Y, so M's zeros (s > t) meet every x of the
 // block. In a block with a NaN or infinity in x, Y is formed with zeros in
 // their place and they are added for t >= s on the CUDA cores, so that no
