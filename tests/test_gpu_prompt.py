@@ -536,3 +536,88 @@ def test_stage_prefill_matches_steps(before, T, after):
     for a, b in zip(one.ssm, many.ssm):
         assert rssm.rssm_get_error(b["state"]) == 0
     assert many.t == one.t
+
+
+# ------------------------------------------------- far offsets, other streams
+
+def test_rows_past_32_bits():
+    """The last of 600000 rows (more than 2^31 elements before them) come out
+    as in a call of their own, for every call."""
+    H, P, N, G, n, T = 64, 64, 128, 8, 300, 600000
+    g = torch.Generator(device="cuda").manual_seed(91)
+    lens = [T - n, n]
+    cu, cu1 = bounds(lens), bounds([n])
+    desc, one = rssm.make_desc(2, H, P, N, G), rssm.make_desc(1, H, P, N, G)
+    din, gn = H * P, G * N
+    rn = lambda *s, t=BF: torch.randn(*s, generator=g, device="cuda", dtype=t)
+    zx = torch.zeros(T, 2 * din + 2 * gn + H, dtype=BF, device="cuda")
+    zx[-2 * n:] = rn(2 * n, zx.shape[1])
+    w, b, dtb, nw = rn(din + 2 * gn, 4, t=F32), rn(din + 2 * gn, t=F32), rn(H, t=F32) - 3, rn(din, t=F32)
+    state = rn(2, 3, din + 2 * gn)
+    keep = state.clone()
+
+    def outs(rows):
+        return (torch.zeros(rows, H, P, dtype=BF, device="cuda"), torch.zeros(rows, G, N, dtype=BF, device="cuda"),
+                torch.zeros(rows, G, N, dtype=BF, device="cuda"), torch.zeros(rows, H, device="cuda"))
+    full, last = outs(T), outs(n)
+    rssm_stage_conv_prompt(desc, cu, zx, state, w, b, dtb, *full)
+    st1 = keep[1:].clone()
+    rssm_stage_conv_prompt(one, cu1, zx[-n:], st1, w, b, dtb, *last)
+    for a, c in zip(full, last):
+        assert torch.equal(a[-n:], c)
+    assert torch.equal(state[1:], st1)
+    A, D = -torch.rand(H, generator=g, device="cuda") - 0.5, rn(H, t=F32)
+    y, y1 = torch.zeros(T, H, P, device="cuda"), torch.zeros(n, H, P, device="cuda")
+    s2, s1 = rssm.RssmState(desc), rssm.RssmState(one)
+    rssm.rssm_prefill_scan(s2, cu, lens[0], *full, A, D, y)
+    rssm.rssm_prefill_scan(s1, cu1, n, *last, A, D, y1)
+    assert rssm.rssm_get_error(s2) == 0 and rssm.rssm_get_error(s1) == 0
+    near(to_np(y[-n:]), to_np(y1), "scan")  # (the long prompt's call may cut in segments)
+    near(to_np(s2.ckpt[1]), to_np(s1.ckpt[0]), "scan's state")
+    del full
+    out, out1 = torch.zeros(T, din, dtype=BF, device="cuda"), torch.zeros(n, din, dtype=BF, device="cuda")
+    rssm_stage_gate_norm_prompt(desc, y, zx, nw, 1e-5, out)
+    rssm_stage_gate_norm_prompt(one, y[-n:], zx[-n:], nw, 1e-5, out1)
+    assert torch.equal(out[-n:], out1)
+    u, u1 = zx.new_zeros(T, din), zx.new_zeros(n, din)
+    n1, n2 = torch.zeros_like(out), torch.zeros_like(out1)
+    rssm_stage_add_norm(u, out, nw, 1e-5, n1, post_w=nw)
+    rssm_stage_add_norm(u1, out1, nw, 1e-5, n2, post_w=nw)
+    assert torch.equal(n1[-n:], n2) and torch.equal(u[-n:], u1)
+
+
+def test_scan_beside_other_tensor_memory_kernels():
+    """The scan on one stream, the tcgen05 prefill and the refresh on others,
+    all holding tensor memory on the same SMs: each result as alone."""
+    shape = LayerShape(64, 8, 64, 128, 2)
+    p = Packed(shape, [200] * 64, 95)
+    inp = make_inputs(shape, 200, 96, BF, device="cuda")
+    ref = p.run()
+    y0 = p.y.clone()
+    a = rssm.RssmState(desc_for(shape))
+    rssm.rssm_prefill(a, inp["x"], inp["B"], inp["dt"], inp["A"])
+    fd = desc_for(shape, update_dtype=rssm.RSSM_BF16, out_copy=rssm.RSSM_OUTCOPY_FP4, seed=3)
+
+    def refreshed(stream=None):
+        f = rssm.RssmState(fd)
+        f.ckpt.copy_(inp["ckpt"].to(BF))
+        torch.cuda.synchronize()
+        for _ in range(4):
+            rssm.rssm_lowprec_refresh(f, inp["A"], force=True, stream=stream)
+        return f
+    f0 = refreshed()
+    s = [torch.cuda.Stream() for _ in range(3)]
+    b, st = rssm.RssmState(desc_for(shape)), p.state()
+    f1 = rssm.RssmState(fd)
+    f1.ckpt.copy_(inp["ckpt"].to(BF))
+    p.y.zero_()
+    torch.cuda.synchronize()
+    for _ in range(4):
+        rssm.rssm_lowprec_refresh(f1, inp["A"], force=True, stream=s[2])
+    rssm.rssm_prefill_scan(st, p.cu, 200, p.x, p.B, p.C, p.dt, p.A, p.D, p.y, stream=s[0])
+    rssm.rssm_prefill(b, inp["x"], inp["B"], inp["dt"], inp["A"], stream=s[1])
+    torch.cuda.synchronize()
+    assert torch.equal(p.y[:12800], y0[:12800]) and torch.equal(st.ckpt, ref.ckpt)
+    assert torch.equal(b.ckpt, a.ckpt) and torch.equal(f1.ckpt, f0.ckpt)
+    for q in (st, b, f0, f1):
+        assert rssm.rssm_get_error(q) == 0
