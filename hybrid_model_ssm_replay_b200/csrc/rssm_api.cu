@@ -297,7 +297,7 @@ rssm_status_t rssm_prefill(const rssm_desc_t* d, const rssm_state_t* st, int32_t
 }
 
 size_t rssm_prefill_scan_workspace_bytes(const rssm_desc_t* d, int32_t total, int32_t max_seqlen) {
-    if (rssm_check_desc(d) != RSSM_OK || total <= 0 || max_seqlen <= 0) return 0;
+    if (rssm_check_desc(d) != RSSM_OK || total <= 0 || total > RSSM_PROMPT_TOKENS_MAX || max_seqlen <= 0) return 0;
     const Shape s = shape_of(d);
     return scan_workspace_bytes(s, total, scan_segment_len(s, d->in_dtype == RSSM_BF16, total, max_seqlen));
 }
@@ -310,7 +310,7 @@ rssm_status_t rssm_prefill_scan(const rssm_desc_t* d, const rssm_state_t* st, in
     if (s != RSSM_OK) return s;
     if (d->update_dtype != RSSM_F32 || d->out_copy != RSSM_OUTCOPY_NONE) return RSSM_ERR_UNSUPPORTED;
     if (!st || !st->record || !st->pos || !st->err || !cu_seqlens) return RSSM_ERR_INVALID_ARG;
-    if (total < 0 || max_seqlen < 0) return RSSM_ERR_INVALID_ARG;
+    if (total < 0 || total > RSSM_PROMPT_TOKENS_MAX || max_seqlen < 0) return RSSM_ERR_INVALID_ARG;
     if (total > 0 && (!x || !B || !C || !dt || !A || !D || !y)) return RSSM_ERR_INVALID_ARG;
     if (!aligned16({x, B, C, dt, A, D, y, workspace})) return RSSM_ERR_INVALID_ARG;
     if (total == 0) return RSSM_OK;

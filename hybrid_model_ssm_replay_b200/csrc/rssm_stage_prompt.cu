@@ -675,7 +675,7 @@ rssm_status_t rssm_stage_conv_prompt(const rssm_desc_t* d, int32_t total, const 
                                      void* stream) {
     rssm_status_t s = prompt_shape_ok(d);
     if (s != RSSM_OK) return s;
-    if (total < 0 || !cu_seqlens || !conv_state || !conv_w || !conv_b || !dt_bias) return RSSM_ERR_INVALID_ARG;
+    if (total < 0 || total > RSSM_PROMPT_TOKENS_MAX || !cu_seqlens || !conv_state || !conv_w || !conv_b || !dt_bias) return RSSM_ERR_INVALID_ARG;
     if (total == 0) return RSSM_OK;
     if (!zxbcdt || !x || !B || !C || !dt) return RSSM_ERR_INVALID_ARG;
     if (!aligned16({zxbcdt, conv_state, conv_w, conv_b, dt_bias, x, B, C, dt})) return RSSM_ERR_INVALID_ARG;
@@ -701,7 +701,7 @@ rssm_status_t rssm_stage_conv_prompt(const rssm_desc_t* d, int32_t total, const 
     const bool vec = a.din % 4 == 0 && a.gn % 4 == 0 && a.H % 4 == 0;
     const int per_cta = (vec ? 4 : 1) * kConvThreads;
     const int ny = (chans + per_cta - 1) / per_cta + 1;  // and the dt heads
-    if (ny > 65535) return RSSM_ERR_SHAPE;
+    if (ny > 65535 || a.H > 1 << 23) return RSSM_ERR_SHAPE;  // (a CTA's dt values are counted in an int)
     // Tokens per CTA: 128 (three rows before them are read again, and the
     // weights once per CTA; 778 us at 32, 714 us at 128 for 256 x 512 tokens),
     // fewer while that leaves SMs without work

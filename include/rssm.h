@@ -289,7 +289,11 @@ RSSM_API rssm_status_t rssm_prefill(const rssm_desc_t *desc, const rssm_state_t 
  * cu_seqlens[b] .. cu_seqlens[b+1]-1 of every per-token array; cu_seqlens is
  * a device int32 [batch+1], not decreasing, within 0..total. A request may
  * have no tokens. Rows of no request (before cu_seqlens[0], from
- * cu_seqlens[batch] on) are not written, and what they hold does not matter. */
+ * cu_seqlens[batch] on) are not written, and what they hold does not matter.
+ * A call takes at most RSSM_PROMPT_TOKENS_MAX rows. Where cu_seqlens decreases
+ * (an error, below) the requests beside the bad ones may not have run either:
+ * their results do not count. */
+#define RSSM_PROMPT_TOKENS_MAX 0x7fffff00
 
 /* Selective scan of packed prompts with their outputs -- the prefill of a
  * layer whose outputs the next layer needs (the article is silent on it):
@@ -316,7 +320,7 @@ RSSM_API rssm_status_t rssm_prefill(const rssm_desc_t *desc, const rssm_state_t 
  * A NaN or infinity in the inputs of a token reaches that token and later
  * ones of its request (of x: in its head_dim column), none before it.
  * Requires an fp32 state (update_dtype F32, no output copy), else
- * RSSM_ERR_UNSUPPORTED; total, max_seqlen >= 0. A workspace too small:
+ * RSSM_ERR_UNSUPPORTED; 0 <= total <= RSSM_PROMPT_TOKENS_MAX, max_seqlen >= 0. A workspace too small:
  * RSSM_ERR_CAPACITY. Device errors: pos[b] != 0; a bad cu_seqlens range or a
  * prompt longer than max_seqlen. That request is left untouched. */
 RSSM_API rssm_status_t rssm_prefill_scan(const rssm_desc_t *desc, const rssm_state_t *state, int32_t total,

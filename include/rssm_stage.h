@@ -74,7 +74,7 @@ RSSM_API rssm_status_t rssm_stage_gate_norm(const rssm_desc_t *desc, const float
  *   x [total][H][P], B and C [total][G][N] bf16; dt [total][H] float
  *   conv_state, conv_w, conv_b, dt_bias as in rssm_stage_conv
  *   err     device int32, the error word (state->err), or NULL
- * total >= 0. Device error: a bad cu_seqlens range (RSSM_DEVERR_SEQ_RANGE;
+ * 0 <= total <= RSSM_PROMPT_TOKENS_MAX; nheads <= 2^23. Device error: a bad cu_seqlens range (RSSM_DEVERR_SEQ_RANGE;
  * that request is left untouched). */
 RSSM_API rssm_status_t rssm_stage_conv_prompt(const rssm_desc_t *desc, int32_t total, const int32_t *cu_seqlens,
                                               const void *zxbcdt, void *conv_state, const float *conv_w,

@@ -130,3 +130,12 @@ def test_stage_prefill_needs_the_replay_scheme():
         s.prefill(torch.zeros(2, 3, 64))
     with pytest.raises(ValueError, match="cache"):
         s.prefill(torch.zeros(2, 9, 64, dtype=torch.bfloat16))
+
+
+def test_sizes_past_32_bit_counters_are_refused(L):
+    """Row numbers go 128 past a call's last row, a CTA's dt values are one int."""
+    st = rssm.StateStruct(*([0x1000] * 7))
+    assert scan(L, cfg(), st, total=0x7fffff01) == INVALID
+    assert rssm.rssm_prefill_scan_workspace_bytes(cfg(batch=1), 0x7fffff01, 0x7fffffff) == 0
+    assert conv(L, cfg(), total=0x7fffff01) == INVALID
+    assert conv(L, cfg(nheads=1 << 24, head_dim=1, d_state=1, ngroups=1)) == SHAPE
