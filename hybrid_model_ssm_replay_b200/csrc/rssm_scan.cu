@@ -636,7 +636,11 @@ __global__ void __launch_bounds__(kSuThreads, 2)
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         su_fence_before();
-        if (__syncthreads_or(timed_out)) break;  // the block, its decays and the state's parts are in place
+        if (__syncthreads_or(timed_out)) {  // (x, where its copy is under way, lands before the CTA ends)
+            if (!OUT || t0 == it.t0) su_wait_long(bar_x, par);
+            break;
+        }
+        // the block, its decays and the state's parts are in place
         su_fence_after();
         if (OUT && warp == kSuStorer && t0 != it.t0) {
             if (elect_one()) {  // Y of the block before has left x's buffer
