@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace rssm {
 
 enum Fmt : int { kF32 = 0, kBF16 = 1, kE4M3 = 2, kFP4 = 3 };
@@ -174,5 +176,18 @@ size_t fold_smem_bytes(const Shape& s, int upd_fmt);
 // Record geometry for the read-copy format and the input element size.
 RecLayout record_layout(const Shape& s, int read_fmt, int in_bytes);
 size_t conv_smem_bytes(const Shape& s);
+
+// Lets a kernel use `bytes` of dynamic shared memory, once per device.
+template <typename K>
+cudaError_t allow_smem(K kernel, size_t bytes, std::atomic<uint64_t>& done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev >= 0 && dev < 64 ? 1ull << dev : 0;
+    if (bit && (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+    return e;
+}
 
 }  // namespace rssm

@@ -1094,19 +1094,6 @@ bool encode_out(CUtensorMap* m, float* base, int total, int H, int P) {
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Lets a kernel use `bytes` of dynamic shared memory, once per device.
-template <typename K>
-cudaError_t allow_smem(K kernel, size_t bytes, std::atomic<uint64_t>& done) {
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    const uint64_t bit = dev >= 0 && dev < 64 ? 1ull << dev : 0;
-    if (bit && (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
-    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
-    return e;
-}
-
 template <bool OUT>
 cudaError_t launch_umma(const ScanArgs& a, int items, cudaStream_t st) {
     const int slices = (a.s.P + 63) / 64;

@@ -10,6 +10,7 @@
 #include <cuda_runtime.h>
 
 #include "rssm.h"
+#include "rssm_internal.h"
 #include "rssm_stage.h"
 
 namespace {
@@ -443,7 +444,23 @@ template <> struct Eight<__nv_bfloat16> {
     uint4 u;
     __device__ __forceinline__ void zero() { u = make_uint4(0, 0, 0, 0); }
     __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = *reinterpret_cast<const uint4*>(p); }
+    __device__ __forceinline__ void load(const uint4* p, int) { u = *p; }  // 16-byte parts so far apart
     __device__ __forceinline__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = u; }
+    // elements lo .. hi - 1, where lo is 0 or hi is 8
+    __device__ __forceinline__ void store_part(__nv_bfloat16* p, int lo, int hi) const {
+        const int n = hi - lo;
+        if (n & 4) *reinterpret_cast<uint2*>(p + (lo ? 4 : 0)) = lo ? make_uint2(u.z, u.w) : make_uint2(u.x, u.y);
+        const bool far = lo ? !(n & 4) : n & 4;  // what is left lies in the second half
+        if (n & 2) {
+            const int i = lo ? (n & 4 ? 2 : 6) : n & 4;
+            *reinterpret_cast<uint32_t*>(p + i) = lo ? (far ? u.w : u.y) : (far ? u.z : u.x);
+        }
+        if (n & 1) {
+            const int i = lo ? lo : hi - 1;
+            const uint32_t w = i < 4 ? (i < 2 ? u.x : u.y) : (i < 6 ? u.z : u.w);
+            p[i] = __ushort_as_bfloat16(static_cast<uint16_t>(i & 1 ? w >> 16 : w));
+        }
+    }
     __device__ __forceinline__ void get(float (&f)[8]) const {
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
@@ -460,9 +477,25 @@ template <> struct Eight<float> {
         a = reinterpret_cast<const float4*>(p)[0];
         b = reinterpret_cast<const float4*>(p)[1];
     }
+    __device__ __forceinline__ void load(const uint4* p, int step) {
+        a = *reinterpret_cast<const float4*>(p);
+        b = *reinterpret_cast<const float4*>(p + step);
+    }
     __device__ __forceinline__ void store(float* p) const {
         reinterpret_cast<float4*>(p)[0] = a;
         reinterpret_cast<float4*>(p)[1] = b;
+    }
+    __device__ __forceinline__ void store_part(float* p, int lo, int hi) const {  // where lo is 0 or hi is 8
+        const int n = hi - lo;
+        if (n & 4) *reinterpret_cast<float4*>(p + (lo ? 4 : 0)) = lo ? b : a;
+        const bool far = lo ? !(n & 4) : n & 4;  // what is left lies in the second half
+        const float4 q = far ? b : a;
+        const int base = far ? 4 : 0;
+        if (n & 2) *reinterpret_cast<float2*>(p + base + (lo ? 2 : 0)) = lo ? make_float2(q.z, q.w) : make_float2(q.x, q.y);
+        if (n & 1) {
+            const int i = (lo ? lo : hi - 1) & 3;
+            p[base + i] = i < 2 ? (i ? q.y : q.x) : (i > 2 ? q.w : q.z);
+        }
     }
     __device__ __forceinline__ void get(float (&f)[8]) const {
         f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
@@ -565,10 +598,195 @@ __global__ void __launch_bounds__(512) k_add_norm_rows(const AddNormArgs a, cons
     }
 }
 
-// Any other width: `warps` warps per row, element by element, kAddKeep elements
-// per lane in registers and the rest of a wide row read again. B200, 5003 rows
-// of 2561, fp32 stream (154 MB): 57 us, 0.41 of the copy rate, bound by the
-// latency of the two sums (24 elements per lane: 109 us, 16: 71 us).
+// ---------------------------------------------------------------------------
+// Any other width from 9 to kShiftDim: a row starts at any of 8 places in a
+// piece of 8 elements (the same one in u, v, u_out and out, which all start on
+// 16 bytes), so a team of warps takes rows that many teams apart, a multiple
+// of 8: its rows all start at the same place. A lane has one piece of a row (K =
+// 2 above 4089 elements: two) with its weights in registers for every row. The
+// next two rows are on their way to shared memory, 16 bytes at a time; the
+// pieces at a row's ends are stored in parts. Bound by instruction issue (63 %
+// busy before pairs of fp32 went through one instruction) and the two sums.
+// B200: 5003 rows of 2561, fp32 stream (154 MB), 41 us, 0.57 of the copy rate;
+// 20000 of 2561, bf16, 111 us (0.57); 200000 of 1001, fp32, 0.54 ms (0.69);
+// 700000 of 257, bf16, 0.67 ms (0.33); 24000 of 8185, fp32, 0.55 ms (0.66).
+// Element by element these took 55, 247, 686, 785 and 1120 us. The next row's
+// pieces in registers instead: 57 and 138 us for the first two.
+// ---------------------------------------------------------------------------
+constexpr int kShiftRows = 3;                      // rows of a team on their way or at work
+constexpr int kShiftHold = 1024;                   // threads per SM
+constexpr int kShiftThreads = 512;
+constexpr int kShiftDim = 16 * kShiftThreads - 7;  // two pieces per thread wherever the row starts
+
+// 16 bytes into shared memory, `n` of them read and the rest zeros.
+__device__ __forceinline__ void copy16(uint4* dst, const void* src, int n) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                     static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+                 "l"(src), "r"(n)
+                 : "memory");
+}
+
+template <typename TU, int K>
+__global__ void __launch_bounds__(kShiftThreads) k_add_norm_shifted(const AddNormArgs a, const int warps) {
+    // partial sums of the teams' warps, two sets in turn (one barrier per sum)
+    __shared__ float4 red[2][8][kShiftThreads / 128];
+    extern __shared__ __align__(16) uint4 sm[];  // [kShiftRows][K][u's 16-byte parts, v][threads]
+    constexpr int kParts = sizeof(TU) / 2, kPer = 16 / sizeof(TU);  // 16-byte parts of u, elements of one
+    const int warp = threadIdx.x >> 5, in_cta = warp / warps, per_cta = blockDim.x / 32 / warps;
+    if (threadIdx.x < sizeof(red) / 16) (&red[0][0][0])[threadIdx.x] = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int team = blockIdx.x * per_cta + in_cta, teams = gridDim.x * per_cta;  // a multiple of 8
+    const int off = static_cast<int>(static_cast<long long>(team) * a.dim & 7);
+    // the pieces' first elements of the row and the parts of them that are the row's
+    const int e0 = 8 * (static_cast<int>(threadIdx.x) - 32 * warps * in_cta) - off, apart = 256 * warps;
+    int lo[K], hi[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        lo[k] = max(0, -(e0 + k * apart));
+        hi[k] = min(8, a.dim - (e0 + k * apart));
+    }
+    auto inside = [&](int k, int i) { return i >= lo[k] && i < hi[k]; };
+    auto whole = [&](int k) { return lo[k] == 0 && hi[k] == 8; };
+    const long long step = static_cast<long long>(teams) * a.dim;
+    // the pieces of the next row on their way to this thread's places in a
+    // buffer, its neighbours' elements too (whatever they are at the time), but
+    // nothing past the last row; zeros where there is no row or no piece
+    long long next = team, at = static_cast<long long>(team) * a.dim + e0, from = at;
+    uint4* const mine = sm + threadIdx.x;
+    const int part = blockDim.x, set = (kParts + 1) * part;
+    auto fetch = [&](int buf) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            int n = 8;  // elements
+            if (next + 1 >= a.rows) n = next < a.rows ? hi[k] : 0;
+            if (lo[k] >= hi[k]) n = 0;
+            const long long i = n ? from + k * apart : 0;
+            uint4* to = mine + (buf * K + k) * set;
+            copy16(to, static_cast<const TU*>(a.u) + i, min(kPer, n) * static_cast<int>(sizeof(TU)));
+            if constexpr (kParts == 2)
+                copy16(to + part, static_cast<const TU*>(a.u) + i + (n > kPer ? kPer : 0),
+                       max(0, n - kPer) * static_cast<int>(sizeof(TU)));
+            if (a.v) copy16(to + kParts * part, a.v + i, 2 * n);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        next += teams;
+        from += step;
+    };
+#pragma unroll
+    for (int i = 0; i < kShiftRows - 1; ++i) fetch(i);
+    float2 post[K][4], pre[K][4];  // post_w times gate; pre_w
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        float p[8], q[8];
+        const int e = e0 + k * apart;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            p[i] = a.v && a.post_w && inside(k, i) ? a.post_w[e + i] : 1.f;
+            if (a.v && a.gate && inside(k, i)) p[i] *= a.gate[e + i];
+            q[i] = a.out && inside(k, i) ? a.pre_w[e + i] : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            post[k][i] = make_float2(p[2 * i], p[2 * i + 1]);
+            pre[k][i] = make_float2(q[2 * i], q[2 * i + 1]);
+        }
+    }
+    const float inv_n = 1.0f / static_cast<float>(a.dim);
+    const float2 scale = make_float2(a.scale, a.scale);
+    const float* sums = reinterpret_cast<const float*>(red[0][in_cta]);
+    int turn = 0;
+    auto norm = [&](const float2(&f)[K][4]) {  // 1 / sqrt(mean of the row's squares + eps)
+        float2 s2 = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s2 = fma2(f[k][i], f[k][i], s2);
+        float v = warp_sum(s2.x + s2.y);
+        if (warps > 1) {
+            if ((threadIdx.x & 31) == 0) const_cast<float*>(sums)[turn + warp - in_cta * warps] = v;
+            __syncthreads();
+            const float4* r = reinterpret_cast<const float4*>(sums + turn);
+            v = 0.f;
+            for (int i = 0; i < (warps + 3) / 4; ++i) v += (r[i].x + r[i].y) + (r[i].z + r[i].w);
+            turn ^= 8 * kShiftThreads / 32;
+        }
+        return rsqrtf(v * inv_n + a.eps);
+    };
+    auto pairs = [&](const auto& r, float2(&f)[4]) {
+        float g[8];
+        r.get(g);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = make_float2(g[2 * i], g[2 * i + 1]);
+    };
+    auto get = [&](const auto& r, int k, float2(&f)[4]) {  // zeros outside the row
+        pairs(r, f);
+        if (!whole(k))
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                f[i] = make_float2(inside(k, 2 * i) ? f[i].x : 0.f, inside(k, 2 * i + 1) ? f[i].y : 0.f);
+    };
+    auto set8 = [&](auto& r, const float2(&f)[4]) {
+        const float g[8] = {f[0].x, f[0].y, f[1].x, f[1].y, f[2].x, f[2].y, f[3].x, f[3].y};
+        r.set(g);
+    };
+    auto store = [&](const auto& r, int k, auto* p) {
+        if (whole(k))
+            r.store(p + at + k * apart);
+        else if (lo[k] < hi[k])
+            r.store_part(p + at + k * apart, lo[k], hi[k]);
+    };
+    int buf = 0;
+    __syncthreads();  // red is zeros
+    for (long long row = team, first = static_cast<long long>(blockIdx.x) * per_cta; first < a.rows;
+         first += teams, row += teams, at += step) {  // every team of the CTA goes round together
+        asm volatile("cp.async.wait_group %0;" ::"n"(kShiftRows - 2) : "memory");
+        Eight<TU> u[K];
+        Eight<__nv_bfloat16> v[K];
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const uint4* here = mine + (buf * K + k) * set;
+            u[k].load(here, part);
+            if (a.v) v[k].load(here + kParts * part, part);
+        }
+        buf = buf == 0 ? kShiftRows - 1 : buf - 1;  // where the row before was
+        fetch(buf);
+        buf = buf + 2 >= kShiftRows ? buf + 2 - kShiftRows : buf + 2;
+        float2 f[K][4], g[K][4];
+#pragma unroll
+        for (int k = 0; k < K; ++k) get(u[k], k, g[k]);
+        if (a.v) {
+#pragma unroll
+            for (int k = 0; k < K; ++k) get(v[k], k, f[k]);
+            const float inv = a.post_w ? norm(f) : 1.f;
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    g[k][i] = fma2(scale, mul2(mul2(f[k][i], make_float2(inv, inv)), post[k][i]), g[k][i]);
+                set8(u[k], g[k]);
+                if constexpr (kParts == 1) pairs(u[k], g[k]);  // as it is kept
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            if (a.u_out && row < a.rows) store(u[k], k, static_cast<TU*>(a.u_out));
+        if (!a.out) continue;
+        const float inv = norm(g);
+        if (row >= a.rows) continue;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            Eight<__nv_bfloat16> o;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) g[k][i] = mul2(mul2(g[k][i], make_float2(inv, inv)), pre[k][i]);
+            set8(o, g[k]);
+            store(o, k, a.out);
+        }
+    }
+}
+
+// The widest and the narrowest rows of other widths: `warps` warps per row,
+// element by element, kAddKeep elements per lane in registers and the rest of
+// a wide row read again. B200, 3000 rows of 12001, fp32 stream (432 MB): 0.29
+// ms, 0.23 of the copy rate.
 constexpr int kAddKeep = 12;
 template <typename TU>
 __global__ void __launch_bounds__(kNormThreads) k_add_norm_any(const AddNormArgs a, const int warps) {
@@ -675,7 +893,8 @@ rssm_status_t rssm_stage_conv_prompt(const rssm_desc_t* d, int32_t total, const 
                                      void* stream) {
     rssm_status_t s = prompt_shape_ok(d);
     if (s != RSSM_OK) return s;
-    if (total < 0 || total > RSSM_PROMPT_TOKENS_MAX || !cu_seqlens || !conv_state || !conv_w || !conv_b || !dt_bias) return RSSM_ERR_INVALID_ARG;
+    if (total < 0 || total > RSSM_PROMPT_TOKENS_MAX || !cu_seqlens || !conv_state || !conv_w || !conv_b || !dt_bias)
+        return RSSM_ERR_INVALID_ARG;
     if (total == 0) return RSSM_OK;
     if (!zxbcdt || !x || !B || !C || !dt) return RSSM_ERR_INVALID_ARG;
     if (!aligned16({zxbcdt, conv_state, conv_w, conv_b, dt_bias, x, B, C, dt})) return RSSM_ERR_INVALID_ARG;
@@ -782,6 +1001,26 @@ rssm_status_t rssm_stage_add_norm(int32_t rows, int32_t dim, int32_t u_dtype, co
             k_add_norm_rows<float><<<grid, threads, 0, st>>>(a, warps);
         else
             k_add_norm_rows<__nv_bfloat16><<<grid, threads, 0, st>>>(a, warps);
+    } else if (dim > 8 && dim <= kShiftDim) {
+        const bool two = dim > 8 * kShiftThreads - 7;
+        const int warps = (dim + 7 + (two ? 511 : 255)) / (two ? 512 : 256), per_cta = warps < 8 ? 8 / warps : 1;
+        const int threads = 32 * warps * per_cta;
+        // teams a multiple of 8, no more than the GPU holds (a few CTAs more would run
+        // alone at the end) or there are rows
+        const long long unit = per_cta % 8 == 0 ? 1 : per_cta % 4 == 0 ? 2 : per_cta % 2 == 0 ? 4 : 8;
+        const long long want = (rows - 1ll + unit * per_cta) / (unit * per_cta);
+        const long long hold = static_cast<long long>(sm_count()) * (kShiftHold / threads) / unit;
+        const unsigned grid = static_cast<unsigned>(unit * (want < hold ? want : hold > 0 ? hold : 1));
+        const size_t piece = u_dtype == RSSM_F32 ? 48 : 32;
+        auto go = [&](auto kernel, std::atomic<uint64_t>& done) {
+            if (rssm::allow_smem(kernel, kShiftRows * kShiftThreads * 2 * 48, done) != cudaSuccess) return RSSM_ERR_CUDA;
+            kernel<<<grid, threads, kShiftRows * threads * piece * (two ? 2 : 1), st>>>(a, warps);
+            return launched();
+        };
+        static std::atomic<uint64_t> done[4];
+        if (u_dtype == RSSM_F32)
+            return two ? go(k_add_norm_shifted<float, 2>, done[0]) : go(k_add_norm_shifted<float, 1>, done[1]);
+        return two ? go(k_add_norm_shifted<__nv_bfloat16, 2>, done[2]) : go(k_add_norm_shifted<__nv_bfloat16, 1>, done[3]);
     } else {
         int warps = 1;  // per row, the elements that lanes keep
         while (warps < kNormThreads / 32 && 32 * kAddKeep * warps < dim) warps *= 2;

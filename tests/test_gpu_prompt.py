@@ -492,6 +492,29 @@ def test_add_norm_matches_reference(rows, dim, stream, post, gate):
     assert torch.equal(n, n2)
 
 
+@pytest.mark.parametrize("stream", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("rows,dim", [(20011, 1), (20011, 12), (9001, 257), (5003, 2561), (1500, 4089), (1501, 4090),
+                                      (700, 5001), (800, 8185), (300, 8186)])
+def test_add_norm_many_odd_rows(rows, dim, stream):
+    """Rows that start at every place of a 16-byte piece, more of them than
+    run at once, in place, with what lies behind the last one left alone."""
+    g = torch.Generator(device="cuda").manual_seed(dim)
+    rn = lambda *s: torch.randn(*s, generator=g, device="cuda")
+    guard = lambda t: torch.cat([t.flatten(), torch.full((64,), 7.0, dtype=t.dtype, device="cuda")])
+    ub, vb = guard((3 * rn(rows, dim)).to(stream)), rn(rows, dim).to(BF)
+    u, pw, gw, w = ub[:-64].view(rows, dim), 1 + 0.1 * rn(dim), rn(dim), 1 + 0.1 * rn(dim)
+    nb, eps, u0 = guard(torch.zeros_like(vb)), 1e-5, u.double()
+    v, n = vb, nb[:-64].view(rows, dim)
+    rssm_stage_add_norm(u, v, w, eps, n, post_w=pw, gate=gw, scale=0.37)
+    assert (ub[-64:] == 7).all() and (nb[-64:] == 7).all()
+    r = v.double()
+    r = 0.37 * r / (r.square().mean(-1, keepdim=True) + eps).sqrt() * pw.double() * gw.double()
+    half = 2.0 ** -8 if stream == BF else 2.0 ** -24
+    assert ((u.double() - u0 - r).abs() <= half * (u0 + r).abs() + 2e-6 * (u0.abs() + r.abs())).all()
+    k = u.double()
+    check_bf16(n, to_np(k / (k.square().mean(-1, keepdim=True) + eps).sqrt() * w.double()), "norm before")
+
+
 def test_add_norm_special_rows():
     """A row of zeros, one of huge values, and one with a NaN that stays in it."""
     u = torch.randn(4, 512, device="cuda").to(BF)
