@@ -957,8 +957,8 @@ rssm_status_t rssm_stage_gate_norm_prompt(const rssm_desc_t* d, int32_t rows, co
         // as the GPU holds (8 CTAs per SM), no more than there are rows
         const long long unit = per_cta % G == 0 ? 1 : G, rows_per_unit = unit * per_cta / G;
         const long long want = (rows + rows_per_unit - 1) / rows_per_unit;
-        const long long hold = (8ll * sm_count() + unit - 1) / unit;
-        const long long units = want < hold ? want : hold;
+        const long long hold = 8ll * sm_count() / unit;
+        const long long units = want < hold ? want : hold > 0 ? hold : 1;
         k_gate_norm_rows<<<static_cast<unsigned>(units * unit), kNormThreads, 0, st>>>(rows, gs, G, warps, Dp, y, zx,
                                                                                        norm_w, eps, o);
         return launched();
