@@ -146,11 +146,14 @@ __device__ __forceinline__ int first_request(const int32_t* cu, int batch, int t
 // lie past its own tokens (the next CTA leaves them out), and it writes the
 // state's new rows, the request's last three inputs, from the projection's
 // rows. Each input row is read once plus three rows of a CTA's tokens before
-// (from L2), each output written once; four channels per thread and four rows
-// fetched ahead (eight channels 1.06 ms, two 0.80 ms in the same case). B200,
-// 256 prompts of 512 tokens, 6144 channels (3.29 GB): 0.75 ms, 0.67 of the
-// copy rate, bound by the latency of its loads and, next, by instruction issue
-// (17 per element; 0.64 ms without silu).
+// (from L2), each output written once. Four channels per thread come through
+// shared memory, 8 bytes of each row by the thread that works on them, a group
+// of four rows at work and two on their way; three CTAs of 80 registers per SM
+// (four of 64 spill: 0.660 ms for the case below, but 42 us for 16 prompts of 1
+// to 1501 tokens, where three take 38 us). B200, 256 prompts of 512 tokens,
+// 6144 channels (3.29 GB): 0.657 ms in bursts, 0.76 of the copy rate; 0.71 ms
+// with the next rows in registers, 0.77 ms with eight channels. Bound by
+// instruction issue (17 per element, 5 of them silu's) and latency.
 // ---------------------------------------------------------------------------
 // What a thread of k_conv_prompt has of its channels: VEC as one load brings
 // them, as floats, and the products.
@@ -170,10 +173,11 @@ template <> struct Chans<1> {
 };
 
 template <int VEC>
-__global__ void __launch_bounds__(kConvThreads, 4) k_conv_prompt(const ConvPromptArgs a) {
+__global__ void __launch_bounds__(kConvThreads, 3) k_conv_prompt(const ConvPromptArgs a) {
     using Raw = typename Chans<VEC>::Raw;
     constexpr int kPairs = (VEC + 1) / 2;
-    constexpr int kAhead = 4;  // rows fetched before the ones at work
+    constexpr int kAhead = 4;  // rows fetched together
+    constexpr int kRing = 3;   // such groups, one at work
     const int chans = a.din + 2 * a.gn;
     const size_t Dp = static_cast<size_t>(a.din) + chans + a.H;
     const int t0 = blockIdx.x * a.tok, t1 = min(a.total - t0, a.tok) + t0;
@@ -222,6 +226,8 @@ __global__ void __launch_bounds__(kConvThreads, 4) k_conv_prompt(const ConvPromp
         dst = a.C + (c - a.din - a.gn);
         width = a.gn;
     }
+    __shared__ Raw ring[VEC == 4 ? kRing * kAhead * kConvThreads : 1];
+    const uint32_t mine = static_cast<uint32_t>(__cvta_generic_to_shared(ring + threadIdx.x));
     auto row = [&](int t) { return *reinterpret_cast<const Raw*>(in + static_cast<size_t>(t) * Dp); };
     for (int r = request0; r < a.batch; ++r) {
         const int s = a.cu[r], e = a.cu[r + 1];
@@ -252,13 +258,6 @@ __global__ void __launch_bounds__(kConvThreads, 4) k_conv_prompt(const ConvPromp
         }
         const __nv_bfloat16* from_x = in + static_cast<size_t>(from) * Dp;   // the next row to fetch
         __nv_bfloat16* to_y = dst + static_cast<size_t>(from) * width;      // the next token's results
-        Raw next[kAhead];
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k)
-            if (from + k < to) {
-                next[k] = *reinterpret_cast<const Raw*>(from_x);
-                from_x += Dp;
-            }
         auto token = [&](const Raw& raw) {
             Chans<VEC> cur;
             cur.set(raw);
@@ -280,25 +279,71 @@ __global__ void __launch_bounds__(kConvThreads, 4) k_conv_prompt(const ConvPromp
             r1 = r2;
             r2 = cur;
         };
-        int left = to - from;
-#pragma unroll 1
-        for (; left >= 2 * kAhead; left -= kAhead)
+        if constexpr (VEC == 4) {
+            const int n = to - from;
+            int got = 0;  // rows fetched, or asked for past the last
+            auto fetch = [&](int buf) {
 #pragma unroll
-            for (int k = 0; k < kAhead; ++k) {
-                const Raw raw = next[k];
-                next[k] = *reinterpret_cast<const Raw*>(from_x);
+                for (int k = 0; k < kAhead; ++k) {
+                    if (got + k < n)
+                        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(
+                                         mine + (buf * kAhead + k) * 8 * kConvThreads),
+                                     "l"(from_x)
+                                     : "memory");
+                    from_x += Dp;
+                }
+                got += kAhead;
+                asm volatile("cp.async.commit_group;" ::: "memory");
+            };
+#pragma unroll
+            for (int i = 0; i < kRing - 1; ++i) fetch(i);
+            int buf = 0;
+#pragma unroll 1
+            for (int i = 0; i < n; i += kAhead) {
+                asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 2) : "memory");
+                Raw raw[kAhead];
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) raw[k] = ring[(buf * kAhead + k) * kConvThreads + threadIdx.x];
+                fetch(buf == 0 ? kRing - 1 : buf - 1);
+                buf = buf + 1 == kRing ? 0 : buf + 1;
+                if (i + kAhead <= n) {
+#pragma unroll
+                    for (int k = 0; k < kAhead; ++k) token(raw[k]);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < kAhead; ++k)
+                        if (i + k < n) token(raw[k]);
+                }
+            }
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+        } else {  // 2 bytes of a row: by way of registers
+            Raw next[kAhead];
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k)
+                if (from + k < to) {
+                    next[k] = *reinterpret_cast<const Raw*>(from_x);
+                    from_x += Dp;
+                }
+            int left = to - from;
+#pragma unroll 1
+            for (; left >= 2 * kAhead; left -= kAhead)
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) {
+                    const Raw raw = next[k];
+                    next[k] = *reinterpret_cast<const Raw*>(from_x);
+                    from_x += Dp;
+                    token(raw);
+                }
+            left -= kAhead;  // rows not yet fetched
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k)
+                if (k < left + kAhead) token(next[k]);
+#pragma unroll 1
+            for (; left > 0; --left) {
+                const Raw raw = *reinterpret_cast<const Raw*>(from_x);
                 from_x += Dp;
                 token(raw);
             }
-        left -= kAhead;  // rows not yet fetched
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k)
-            if (k < left + kAhead) token(next[k]);
-#pragma unroll 1
-        for (; left > 0; --left) {
-            const Raw raw = *reinterpret_cast<const Raw*>(from_x);
-            from_x += Dp;
-            token(raw);
         }
     }
 }
@@ -921,10 +966,10 @@ rssm_status_t rssm_stage_conv_prompt(const rssm_desc_t* d, int32_t total, const 
     const int per_cta = (vec ? 4 : 1) * kConvThreads;
     const int ny = (chans + per_cta - 1) / per_cta + 1;  // and the dt heads
     if (ny > 65535 || a.H > 1 << 23) return RSSM_ERR_SHAPE;  // (a CTA's dt values are counted in an int)
-    // Tokens per CTA: 128 (three rows before them are read again, and the
-    // weights once per CTA; 778 us at 32, 714 us at 128 for 256 x 512 tokens),
-    // fewer while that leaves SMs without work
-    a.tok = 128;
+    // Tokens per CTA: 256 (three rows before them are read again, and the
+    // weights once per CTA; 697 us at 64, 665 us at 128, 657 us at 256 for
+    // 256 x 512 tokens), fewer while that leaves SMs without work
+    a.tok = 256;
     while (a.tok > 4 && static_cast<long long>((total - 1) / a.tok + 1) * ny < 4ll * sm_count()) a.tok /= 2;
     const dim3 grid(static_cast<unsigned>((total - 1) / a.tok + 1), static_cast<unsigned>(ny));
     if (vec)
