@@ -10,6 +10,7 @@ Functions named rssm_* mirror the C entry points one to one. RssmState
 allocates the per-layer state through PyTorch (the library itself never
 allocates).
 """
+import contextlib
 import ctypes as ct
 import os
 
@@ -300,7 +301,7 @@ def rssm_prefill_scan(state, cu_seqlens, max_seqlen, x, B, C, dt, A, D, y, works
     the fp32 checkpoint (pos must be 0): request b's tokens are rows
     cu_seqlens[b] .. cu_seqlens[b+1]-1 of x, B, C, dt and y. workspace: a uint8
     tensor of rssm_prefill_scan_workspace_bytes(desc, total, max_seqlen), or
-    None to allocate it for the call."""
+    None to allocate it for the call, on the call's stream."""
     d = state.desc
     a, in_dt, f32, dev = _arg, _IN_DT[d.in_dtype], torch.float32, _device(x, "x")
     total, H, P, N, G = x.shape[0], d.nheads, d.head_dim, d.d_state, d.ngroups
@@ -312,9 +313,10 @@ def rssm_prefill_scan(state, cu_seqlens, max_seqlen, x, B, C, dt, A, D, y, works
     if workspace is None:
         need = rssm_prefill_scan_workspace_bytes(d, total, max_seqlen)
         if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
-            if stream is not None:
-                workspace.record_stream(stream)
+            # memory of the stream that uses it: what another stream freed may
+            # still be at work there
+            with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+                workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
     size = 0 if workspace is None else workspace.numel()
     ws = a(workspace, torch.uint8, (size,), "workspace", dev)
     _check(lib().rssm_prefill_scan(ct.byref(d), ct.byref(state.struct), total, int(max_seqlen), *args, ws, size,

@@ -1,0 +1,75 @@
+"""The prompt calls as programs make them: memory that another stream still
+works on. Results are compared bit for bit with those of the calls alone."""
+import pytest
+import torch
+
+from hybrid_model_ssm_replay_b200 import rssm
+from hybrid_model_ssm_replay_b200.inputs import LayerShape, make_inputs
+
+pytestmark = pytest.mark.gpu
+
+BF = torch.bfloat16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from hybrid_model_ssm_replay_b200 import build
+    build.build()
+
+
+class Prompt:
+    """One long prompt of two heads, which the scan cuts into segments."""
+
+    def __init__(self, T, seed):
+        inp = make_inputs(LayerShape(1, 2, 64, 128, 1), T, seed, BF, device="cuda")
+        self.args = [inp[k][:, 0].contiguous() for k in ("x", "B", "C", "dt")] + [inp["A"], inp["D"]]
+        self.desc = rssm.make_desc(1, 2, 64, 128, 1)
+        self.need = rssm.rssm_prefill_scan_workspace_bytes(self.desc, T, T)
+        self.cu, self.T = torch.tensor([0, T], dtype=torch.int32, device="cuda"), T
+
+    def fresh(self):
+        return rssm.RssmState(self.desc), torch.zeros(self.T, 2, 64, device="cuda")
+
+    def run(self, st, y, **kw):
+        rssm.rssm_prefill_scan(st, self.cu, self.T, *self.args, y, **kw)
+
+
+def test_scan_workspace_is_not_what_another_stream_still_uses():
+    """A block freed on the current stream, with work on it still queued, is
+    not taken by a scan on a side stream that nothing makes wait."""
+    p, side = Prompt(6000, 3), torch.cuda.Stream()
+    assert p.need > 0
+    st0, y0 = p.fresh()
+    p.run(st0, y0)
+    st, y = p.fresh()
+    held, copy = (torch.empty(p.need, dtype=torch.uint8, device="cuda") for _ in range(2))
+    held.fill_(1)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)  # about 50 ms
+    copy.copy_(held)
+    del held
+    p.run(st, y, stream=side)
+    torch.cuda.synchronize()
+    assert (copy == 1).all()
+    assert torch.equal(y, y0) and torch.equal(st.ckpt, st0.ckpt)
+
+
+def test_scans_on_two_streams_back_to_back():
+    """A segmented scan on the current stream and at once others on side
+    streams and on the current one again, their inputs ready long before."""
+    ps, sides = [Prompt(T, 5 + T) for T in (20000, 20000, 12000)], [torch.cuda.Stream() for _ in range(2)]
+    alone, out = [p.fresh() for p in ps], [p.fresh() for p in ps]
+    for p, (st, y) in zip(ps, alone):
+        p.run(st, y)
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for st, y in out:
+            st.ckpt.zero_()
+            y.zero_()
+        torch.cuda.synchronize()
+        for p, (st, y), s in zip(ps, out, [None] + sides):
+            p.run(st, y, stream=s)
+        torch.cuda.synchronize()
+        for (st, y), (st0, y0) in zip(out, alone):
+            assert rssm.rssm_get_error(st) == 0
+            assert torch.equal(y, y0) and torch.equal(st.ckpt, st0.ckpt)

@@ -1,0 +1,59 @@
+"""What the bindings of the prompt calls do around the library: which stream a
+workspace belongs to. The library and the tensors' addresses are stand-ins, so
+nothing is launched."""
+import contextlib
+from types import SimpleNamespace
+
+import pytest
+import torch
+
+from hybrid_model_ssm_replay_b200 import rssm
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """Stand-ins for the library (every call answers OK and is recorded) and
+    for the checks that need a device."""
+    done = []
+
+    class Lib:
+        def __getattr__(self, name):
+            def call(*args):
+                done.append((name, args))
+                return 4096 if name.endswith("_bytes") else 0
+            return call
+    monkeypatch.setattr(rssm, "lib", Lib)
+    monkeypatch.setattr(rssm, "_device", lambda t, name: 0)
+    monkeypatch.setattr(rssm, "_arg", lambda t, *a: None if t is None else 0x1000)
+    monkeypatch.setattr(rssm, "_stream", lambda stream=None: None)
+    return done
+
+
+def layer(**kw):
+    base = dict(batch=1, nheads=2, head_dim=64, d_state=128, ngroups=1)
+    base.update(kw)
+    return SimpleNamespace(desc=rssm.make_desc(**base), struct=rssm.StateStruct(),
+                           pos=SimpleNamespace(get_device=lambda: 0, device="cuda:0"))
+
+
+@pytest.mark.parametrize("stream", [None, SimpleNamespace(cuda_stream=7)], ids=["current", "side"])
+def test_workspace_belongs_to_the_stream_that_uses_it(calls, monkeypatch, stream):
+    """Memory freed on one stream may still be at work there: a call on another
+    stream may only take memory of its own stream."""
+    current, taken = [None], []
+
+    @contextlib.contextmanager
+    def on(s):
+        current.append(s)
+        yield
+        current.pop()
+
+    def empty(n, **kw):
+        taken.append(current[-1])
+        return SimpleNamespace(numel=lambda: n, record_stream=lambda s: None)
+    monkeypatch.setattr(torch.cuda, "stream", on)
+    x = torch.zeros(4, 2, 64)
+    monkeypatch.setattr(torch, "empty", empty)
+    rssm.rssm_prefill_scan(layer(), x, 4, x, x, x, x, x, x, x, stream=stream)
+    assert taken == [stream] and current == [None]
+    assert [name for name, _ in calls] == ["rssm_prefill_scan_workspace_bytes", "rssm_prefill_scan"]
