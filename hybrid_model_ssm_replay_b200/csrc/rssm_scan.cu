@@ -1110,26 +1110,33 @@ cudaError_t launch_umma(const ScanArgs& a, int items, cudaStream_t st) {
     return cudaGetLastError();
 }
 
+// Shared memory of k_scan: two buffers of tokens and their outputs. The most
+// that a supported shape takes is at head_dim 256, d_state 64 (65792 bytes).
+constexpr size_t scan_smem(int P, int N) {
+    return 4u * kScanTok * (2 * (2 + ((P + 3) & ~3) + 2 * static_cast<size_t>(N)) + P);
+}
+constexpr size_t kScanSmemMax = scan_smem(256, 64);
+static_assert(scan_smem(128, 128) <= kScanSmemMax, "head_dim * d_state is at most 16384");
+
 template <typename TIn, bool OUT>
 cudaError_t launch_pass(const ScanArgs& a, int items, cudaStream_t st) {
     if (scan_umma_shape(a.s, sizeof(TIn) == 2)) return launch_umma<OUT>(a, items, st);
-    const size_t xs = (a.s.P + 3) & ~3;
-    const size_t smem = 4u * kScanTok * (2 * (2 + xs + 2 * static_cast<size_t>(a.s.N)) + a.s.P);
+    const size_t smem = scan_smem(a.s.P, a.s.N);
     const int passes = (a.s.P * a.s.lpr + kThreads - 1) / kThreads;
     const dim3 grid(static_cast<unsigned>(items) * static_cast<unsigned>(a.s.H));
-    auto go = [&](auto kernel) {
-        if (smem > 48 * 1024) {
-            const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-            if (e != cudaSuccess) return e;
-        }
+    // the limit of every shape at once: another thread's launch of another shape must not lower it
+    static std::atomic<uint64_t> allowed[5];
+    auto go = [&](auto kernel, std::atomic<uint64_t>& done) {
+        const cudaError_t e = allow_smem(kernel, kScanSmemMax, done);
+        if (e != cudaSuccess) return e;
         kernel<<<grid, kThreads, smem, st>>>(a);
         return cudaGetLastError();
     };
-    if (passes <= 1) return go(k_scan<TIn, 1, OUT>);
-    if (passes <= 2) return go(k_scan<TIn, 2, OUT>);
-    if (passes <= 4) return go(k_scan<TIn, 4, OUT>);
-    if (passes <= 8) return go(k_scan<TIn, 8, OUT>);
-    return go(k_scan<TIn, 16, OUT>);
+    if (passes <= 1) return go(k_scan<TIn, 1, OUT>, allowed[0]);
+    if (passes <= 2) return go(k_scan<TIn, 2, OUT>, allowed[1]);
+    if (passes <= 4) return go(k_scan<TIn, 4, OUT>, allowed[2]);
+    if (passes <= 8) return go(k_scan<TIn, 8, OUT>, allowed[3]);
+    return go(k_scan<TIn, 16, OUT>, allowed[4]);
 }
 
 }  // namespace

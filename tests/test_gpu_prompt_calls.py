@@ -1,5 +1,9 @@
 """The prompt calls as programs make them: memory that another stream still
-works on. Results are compared bit for bit with those of the calls alone."""
+works on, two host threads. Results are compared bit for bit with those of the
+calls alone."""
+import ctypes as ct
+import threading
+
 import pytest
 import torch
 
@@ -73,3 +77,33 @@ def test_scans_on_two_streams_back_to_back():
         for (st, y), (st0, y0) in zip(out, alone):
             assert rssm.rssm_get_error(st) == 0
             assert torch.equal(y, y0) and torch.equal(st.ckpt, st0.ckpt)
+
+
+def test_scans_of_two_shapes_from_two_threads():
+    """Two host threads call the same kernel with heads of 256 x 64 and 128 x
+    128, whose shared memory differs: no launch is refused."""
+    L, calls = rssm.lib(), []
+    for P, N in ((256, 64), (128, 128)):
+        inp = make_inputs(LayerShape(1, 1, P, N, 1), 1, 9, torch.float32, device="cuda")
+        st = rssm.RssmState(rssm.make_desc(1, 1, P, N, 1, in_dtype=rssm.RSSM_F32))
+        y, cu = torch.zeros(1, 1, P, device="cuda"), torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+        s = torch.cuda.Stream()
+        keep = [cu] + [inp[k][:, 0].contiguous() for k in ("x", "B", "C", "dt")] + [inp["A"], inp["D"], y]
+        args = (ct.byref(st.desc), ct.byref(st.struct), 1, 1, *[ct.c_void_p(t.data_ptr()) for t in keep], None, 0,
+                ct.c_void_p(s.cuda_stream))
+        calls.append((args, keep, st, s))
+    torch.cuda.synchronize()
+    start, refused = threading.Barrier(2), []
+
+    def go(args):
+        start.wait()
+        refused.extend(r for r in (L.rssm_prefill_scan(*args) for _ in range(20000)) if r)
+    threads = [threading.Thread(target=go, args=(c[0],)) for c in calls]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not refused, f"{len(refused)} launches refused: {set(refused)}"
+    for _, _, st, _ in calls:
+        assert rssm.rssm_get_error(st) == 0
