@@ -191,10 +191,12 @@ __global__ void __launch_bounds__(kConvThreads, 3) k_conv_prompt(const ConvPromp
             const int s = a.cu[r], e = a.cu[r + 1];
             if (s >= t1) break;
             if (s < 0 || e < s || e > a.total) continue;
-            const int from = max(s, t0), n = (min(e, t1) - from) * a.H;
-            for (int i = threadIdx.x; i < n; i += kConvThreads) {
-                const size_t t = from + i / a.H;
-                const int h = i % a.H;
+            const int from = max(s, t0), to = min(e, t1);
+            // (256 tokens of 2^23 heads are 2^31 values)
+            const unsigned n = to > from ? static_cast<unsigned>(to - from) * a.H : 0u;
+            for (unsigned i = threadIdx.x; i < n; i += kConvThreads) {
+                const size_t t = from + i / static_cast<unsigned>(a.H);
+                const unsigned h = i % static_cast<unsigned>(a.H);
                 const float v = bf(a.zx[t * Dp + a.din + chans + h]) + a.dt_bias[h];
                 a.dt[t * a.H + h] = v > 20.0f ? v : log1pf(expf(v));
             }
@@ -966,7 +968,7 @@ rssm_status_t rssm_stage_conv_prompt(const rssm_desc_t* d, int32_t total, const 
     const bool vec = a.din % 4 == 0 && a.gn % 4 == 0 && a.H % 4 == 0;
     const int per_cta = (vec ? 4 : 1) * kConvThreads;
     const int ny = (chans + per_cta - 1) / per_cta + 1;  // and the dt heads
-    if (ny > 65535 || a.H > 1 << 23) return RSSM_ERR_SHAPE;  // (a CTA's dt values are counted in an int)
+    if (ny > 65535 || a.H > 1 << 23) return RSSM_ERR_SHAPE;  // (a CTA counts its dt values in 32 bits)
     // Tokens per CTA: 256 (three rows before them are read again, and the
     // weights once per CTA; 697 us at 64, 665 us at 128, 657 us at 256 for
     // 256 x 512 tokens), fewer while that leaves SMs without work

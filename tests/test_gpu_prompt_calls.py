@@ -1,6 +1,6 @@
 """The prompt calls as programs make them: memory that another stream still
-works on, two host threads. Results are compared bit for bit with those of the
-calls alone."""
+works on, two host threads, the most heads that a call takes. Results are
+compared bit for bit with those of the calls alone, or with the formula."""
 import ctypes as ct
 import threading
 
@@ -9,6 +9,7 @@ import torch
 
 from hybrid_model_ssm_replay_b200 import rssm
 from hybrid_model_ssm_replay_b200.inputs import LayerShape, make_inputs
+from hybrid_model_ssm_replay_b200.stage import rssm_stage_conv_prompt
 
 pytestmark = pytest.mark.gpu
 
@@ -107,3 +108,28 @@ def test_scans_of_two_shapes_from_two_threads():
     assert not refused, f"{len(refused)} launches refused: {set(refused)}"
     for _, _, st, _ in calls:
         assert rssm.rssm_get_error(st) == 0
+
+
+def test_conv_of_the_most_heads_the_call_takes():
+    """256 tokens of 2^23 heads: 2^31 values of dt by one CTA, all of them written."""
+    T, N, heads = 256, 4, 1 << 23
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB")
+    g = torch.Generator(device="cuda").manual_seed(17)
+    chans = heads + 2 * N
+    zx = torch.randn(T, heads + chans + heads, generator=g, device="cuda", dtype=BF)
+    state = torch.zeros(1, 3, chans, dtype=BF, device="cuda")
+    w, b = torch.randn(chans, 4, generator=g, device="cuda"), torch.randn(chans, generator=g, device="cuda")
+    dtb = torch.randn(heads, generator=g, device="cuda")
+    x, dt = torch.zeros(T, heads, 1, dtype=BF, device="cuda"), torch.full((T, heads), -1.0, device="cuda")
+    B, C = (torch.zeros(T, 1, N, dtype=BF, device="cuda") for _ in range(2))
+    cu, err = (torch.tensor(v, dtype=torch.int32, device="cuda") for v in ([0, T], [0]))
+    rssm_stage_conv_prompt(rssm.make_desc(1, heads, 1, N, 1), cu, zx, state, w, b, dtb, x, B, C, dt, err=err)
+    assert int(err) == 0
+    assert torch.equal(state[0], zx[-3:, heads:heads + chans])
+    # softplus of an fp32 sum: its rounding, 2^-24 of v, and a few spacings of log1p and exp
+    for t in (0, 1, 100, T - 1):
+        v = zx[t, heads + chans:].double() + dtb.double()
+        ref = torch.where(v > 20, v, torch.log1p(torch.exp(v)))
+        assert ((dt[t].double() - ref).abs() <= 1e-6 * (ref + v.abs())).all(), t
+    assert (dt >= 0).all()
