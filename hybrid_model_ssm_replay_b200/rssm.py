@@ -143,6 +143,17 @@ def _arg(t, dtype, shape, name, dev):
     return p
 
 
+I32_MAX = (1 << 31) - 1
+
+
+def _rows(t, name):
+    """The rows of a tensor, which the library counts in 32 bits (ctypes would
+    take a larger number modulo 2^32)."""
+    if t.shape[0] > I32_MAX:
+        raise ValueError(f"{name} has {t.shape[0]} rows, more than a call takes")
+    return t.shape[0]
+
+
 def _stream(stream=None):
     if stream is None:  # the current stream's handle, without making a Stream object of it
         return ct.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
@@ -293,7 +304,8 @@ def rssm_prefill(state, x, B, dt, A, stream=None):
 
 
 def rssm_prefill_scan_workspace_bytes(desc, total, max_seqlen):
-    return lib().rssm_prefill_scan_workspace_bytes(ct.byref(desc), int(total), int(max_seqlen))
+    return lib().rssm_prefill_scan_workspace_bytes(ct.byref(desc), min(int(total), I32_MAX),
+                                                   min(int(max_seqlen), I32_MAX))
 
 
 def rssm_prefill_scan(state, cu_seqlens, max_seqlen, x, B, C, dt, A, D, y, workspace=None, stream=None):
@@ -304,7 +316,7 @@ def rssm_prefill_scan(state, cu_seqlens, max_seqlen, x, B, C, dt, A, D, y, works
     None to allocate it for the call, on the call's stream."""
     d = state.desc
     a, in_dt, f32, dev = _arg, _IN_DT[d.in_dtype], torch.float32, _device(x, "x")
-    total, H, P, N, G = x.shape[0], d.nheads, d.head_dim, d.d_state, d.ngroups
+    total, H, P, N, G = _rows(x, "x"), d.nheads, d.head_dim, d.d_state, d.ngroups
     if state.pos.get_device() != dev:
         raise ValueError(f"the state is on {state.pos.device}, the current device is cuda:{dev}")
     args = (a(cu_seqlens, torch.int32, (d.batch + 1,), "cu_seqlens", dev), a(x, in_dt, (total, H, P), "x", dev),
@@ -319,8 +331,8 @@ def rssm_prefill_scan(state, cu_seqlens, max_seqlen, x, B, C, dt, A, D, y, works
                 workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
     size = 0 if workspace is None else workspace.numel()
     ws = a(workspace, torch.uint8, (size,), "workspace", dev)
-    _check(lib().rssm_prefill_scan(ct.byref(d), ct.byref(state.struct), total, int(max_seqlen), *args, ws, size,
-                                   _stream(stream)), "rssm_prefill_scan")
+    _check(lib().rssm_prefill_scan(ct.byref(d), ct.byref(state.struct), total, min(int(max_seqlen), I32_MAX), *args,
+                                   ws, size, _stream(stream)), "rssm_prefill_scan")
     return y
 
 

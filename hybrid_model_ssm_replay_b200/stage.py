@@ -108,7 +108,7 @@ def rssm_stage_conv_prompt(desc, cu_seqlens, zxbcdt, conv_state, conv_w, conv_b,
     and updated. err: the state's error word (RssmState.err), or None."""
     a, bf, f32, dev = rssm._arg, torch.bfloat16, torch.float32, rssm._device(zxbcdt, "zxbcdt")
     H, P, N, G = desc.nheads, desc.head_dim, desc.d_state, desc.ngroups
-    total, chans = zxbcdt.shape[0], H * P + 2 * G * N
+    total, chans = rssm._rows(zxbcdt, "zxbcdt"), H * P + 2 * G * N
     rssm._check(_lib().rssm_stage_conv_prompt(
         ct.byref(desc), total, a(cu_seqlens, torch.int32, (desc.batch + 1,), "cu_seqlens", dev),
         a(zxbcdt, bf, (total, H * P + chans + H), "zxbcdt", dev),
@@ -124,7 +124,7 @@ def rssm_stage_gate_norm_prompt(desc, y, zxbcdt, norm_w, eps, out, stream=None):
     not used); y [rows][d_inner] or [rows][H][P]."""
     a, bf, f32, dev = rssm._arg, torch.bfloat16, torch.float32, rssm._device(zxbcdt, "zxbcdt")
     H, P = desc.nheads, desc.head_dim
-    rows, din = zxbcdt.shape[0], H * P
+    rows, din = rssm._rows(zxbcdt, "zxbcdt"), H * P
     rssm._check(_lib().rssm_stage_gate_norm_prompt(
         ct.byref(desc), rows, a(y, f32, (rows, din) if y.dim() == 2 else (rows, H, P), "y", dev),
         a(zxbcdt, bf, (rows, 2 * din + 2 * desc.ngroups * desc.d_state + H), "zxbcdt", dev),
@@ -140,12 +140,14 @@ def rssm_stage_add_norm(u, v, pre_w, eps, out, post_w=None, gate=None, scale=1.0
     a, bf, f32, dev = rssm._arg, torch.bfloat16, torch.float32, rssm._device(u, "u")
     if u.dim() != 2:
         raise ValueError(f"u has shape {tuple(u.shape)}, expected rows of one width")
-    shape, wide = u.shape, u.shape[1:]
+    shape, wide, rows = u.shape, u.shape[1:], rssm._rows(u, "u")
+    if shape[1] > rssm.I32_MAX:
+        raise ValueError(f"u is {shape[1]} wide, more than a call takes")
     t = f32 if u.dtype == f32 else bf
     up = a(u, t, shape, "u", dev)
     uo = (None if v is None else up) if u_out is None else a(u_out, t, shape, "u_out", dev)
     rssm._check(_lib().rssm_stage_add_norm(
-        shape[0], shape[1], rssm.RSSM_F32 if t == f32 else rssm.RSSM_BF16, up, a(v, bf, shape, "v", dev),
+        rows, shape[1], rssm.RSSM_F32 if t == f32 else rssm.RSSM_BF16, up, a(v, bf, shape, "v", dev),
         a(post_w, f32, wide, "post_w", dev), a(gate, f32, wide, "gate", dev), float(scale),
         a(pre_w, f32, wide, "pre_w", dev), float(eps), uo, a(out, bf, shape, "out", dev), rssm._stream(stream)),
         "rssm_stage_add_norm")

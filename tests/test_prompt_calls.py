@@ -1,13 +1,13 @@
 """What the bindings of the prompt calls do around the library: which stream a
-workspace belongs to. The library and the tensors' addresses are stand-ins, so
-nothing is launched."""
+workspace belongs to, sizes past the library's 32 bits. The library and the
+tensors' addresses are stand-ins, so nothing is launched."""
 import contextlib
 from types import SimpleNamespace
 
 import pytest
 import torch
 
-from hybrid_model_ssm_replay_b200 import rssm
+from hybrid_model_ssm_replay_b200 import rssm, stage
 
 
 @pytest.fixture
@@ -23,6 +23,7 @@ def calls(monkeypatch):
                 return 4096 if name.endswith("_bytes") else 0
             return call
     monkeypatch.setattr(rssm, "lib", Lib)
+    monkeypatch.setattr(stage, "_lib", Lib)
     monkeypatch.setattr(rssm, "_device", lambda t, name: 0)
     monkeypatch.setattr(rssm, "_arg", lambda t, *a: None if t is None else 0x1000)
     monkeypatch.setattr(rssm, "_stream", lambda stream=None: None)
@@ -57,3 +58,27 @@ def test_workspace_belongs_to_the_stream_that_uses_it(calls, monkeypatch, stream
     rssm.rssm_prefill_scan(layer(), x, 4, x, x, x, x, x, x, x, stream=stream)
     assert taken == [stream] and current == [None]
     assert [name for name, _ in calls] == ["rssm_prefill_scan_workspace_bytes", "rssm_prefill_scan"]
+
+
+@pytest.mark.parametrize("n", [1 << 31, (1 << 32) + 3])
+def test_sizes_past_32_bits_are_refused(calls, n):
+    """Not taken modulo 2^32: 2^32 + 3 rows are not three rows."""
+    t = lambda *s, dtype=torch.bfloat16: torch.empty(s, dtype=dtype, device="meta")
+    d = layer(head_dim=1, nheads=1, d_state=16).desc
+    w = t(1)
+    for call in (lambda: stage.rssm_stage_add_norm(t(n, 1), t(n, 1), w, 1e-5, t(n, 1)),
+                 lambda: stage.rssm_stage_add_norm(t(1, n), None, w, 1e-5, t(1, n)),
+                 lambda: stage.rssm_stage_gate_norm_prompt(d, t(n, 1), t(n, 35), w, 1e-5, t(n, 1)),
+                 lambda: stage.rssm_stage_conv_prompt(d, w, t(n, 35), w, w, w, w, w, w, w, w),
+                 lambda: rssm.rssm_prefill_scan(layer(), w, 1, t(n, 2, 64), w, w, w, w, w, w)):
+        with pytest.raises(ValueError, match="rows|wide"):
+            call()
+    assert not calls
+
+
+def test_any_bound_on_the_lengths_is_taken(calls):
+    """A bound past 32 bits still bounds every length."""
+    x = torch.zeros(4, 2, 64)
+    rssm.rssm_prefill_scan(layer(), x, (1 << 32) + 1, x, x, x, x, x, x, x, workspace=x)
+    (name, args), = calls
+    assert name == "rssm_prefill_scan" and args[2:4] == (4, (1 << 31) - 1)
