@@ -288,6 +288,7 @@ class HybridStage:
         if (self.t - self.t0) % s.interval:  # decoded tokens still in the buffers
             for b, st in zip(self.blocks, self.ssm):
                 rssm.rssm_flush(st["state"], b["A"], force=True)
+            self.t0 = self.t  # the buffers are empty, whatever comes of the prompt
         rows, dev = s.batch * T, u.device
         u = u.reshape(rows, s.d_model).clone()
         cu = torch.arange(s.batch + 1, dtype=torch.int32, device=dev) * T

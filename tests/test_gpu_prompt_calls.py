@@ -1,15 +1,16 @@
 """The prompt calls as programs make them: memory that another stream still
 works on, two host threads, the most heads that a call takes. Results are
-compared bit for bit with those of the calls alone, or with the formula."""
+compared bit for bit with those of the calls alone, or with the formula; the
+residual stream of a stage in aggregate, as in its own tests."""
 import ctypes as ct
 import threading
 
 import pytest
 import torch
 
-from hybrid_model_ssm_replay_b200 import rssm
+from hybrid_model_ssm_replay_b200 import rssm, stage
 from hybrid_model_ssm_replay_b200.inputs import LayerShape, make_inputs
-from hybrid_model_ssm_replay_b200.stage import rssm_stage_conv_prompt
+from hybrid_model_ssm_replay_b200.stage import HybridStage, StageShape, make_weights, rssm_stage_conv_prompt
 
 pytestmark = pytest.mark.gpu
 
@@ -133,3 +134,31 @@ def test_conv_of_the_most_heads_the_call_takes():
         ref = torch.where(v > 20, v, torch.log1p(torch.exp(v)))
         assert ((dt[t].double() - ref).abs() <= 1e-6 * (ref + v.abs())).all(), t
     assert (dt >= 0).all()
+
+
+STAGE = StageShape(batch=3, d_model=64, nheads=4, head_dim=32, d_state=64, ngroups=2, interval=16, n_ssm=2, n_attn=1,
+                   attn_heads=2, kv_heads=1, attn_head_dim=32, ctx=24)
+
+
+def test_stage_decodes_on_after_a_prefill_that_failed(monkeypatch):
+    """A prefill that stops right after its flush (no memory for its buffers),
+    after five decoded tokens: the next forty are those of a stage that never
+    tried, over two ends of intervals."""
+    w = make_weights(STAGE, 11)
+    ref, st = HybridStage(STAGE, w, seed=5), HybridStage(STAGE, w, seed=5)
+    g = torch.Generator().manual_seed(9)
+    u = torch.randn(45, STAGE.batch, STAGE.d_model, generator=g).to(BF).cuda()
+
+    def stop(*args, **kw):
+        raise MemoryError
+    for t in range(45):
+        if t == 5:
+            with monkeypatch.context() as m:
+                m.setattr(stage, "rssm_stage_add_norm", stop)
+                with pytest.raises(MemoryError):
+                    st.prefill(u[:3].transpose(0, 1))
+        a, b = ref.step(u[t]).double(), st.step(u[t]).double()
+        d, scale = (a - b).abs(), a.square().mean().sqrt()
+        assert d.square().mean().sqrt() <= 0.01 * scale and d.max() <= 0.05 * scale, t
+    for layer in st.ssm:
+        assert rssm.rssm_get_error(layer["state"]) == 0

@@ -1,6 +1,6 @@
 """What the bindings of the prompt calls do around the library: which stream a
-workspace belongs to, sizes past the library's 32 bits. The library and the
-tensors' addresses are stand-ins, so nothing is launched."""
+workspace belongs to, sizes past the library's 32 bits, a prefill that fails.
+The library and the tensors' addresses are stand-ins, so nothing is launched."""
 import contextlib
 from types import SimpleNamespace
 
@@ -82,3 +82,32 @@ def test_any_bound_on_the_lengths_is_taken(calls):
     rssm.rssm_prefill_scan(layer(), x, (1 << 32) + 1, x, x, x, x, x, x, x, workspace=x)
     (name, args), = calls
     assert name == "rssm_prefill_scan" and args[2:4] == (4, (1 << 31) - 1)
+
+
+class Stop(Exception):
+    pass
+
+
+def bare_stage(monkeypatch, t):
+    """A stage after t decoded tokens whose prefill flushes and then fails, as
+    one without memory for its buffers does; returns it, the flushes it makes
+    and the residual streams that its first norm gets."""
+    s, flushes, streams = stage.HybridStage.__new__(stage.HybridStage), [], []
+    s.shape, s.scheme, s.t, s.t0 = stage.StageShape(2, 64, 4, 16, 16, 1, n_ssm=1, n_attn=0), "replay", t, 0
+    s.blocks, s.attn, s.ssm = [{"A": None, "norm": torch.ones(64)}], [], [{"state": None}]
+
+    def norm(u, *args):
+        streams.append(u)
+        raise Stop
+    monkeypatch.setattr(rssm, "rssm_flush", lambda st, A, force=False: flushes.append(force))
+    monkeypatch.setattr(stage, "rssm_stage_add_norm", norm)
+    return s, flushes, streams
+
+
+def test_intervals_count_from_the_prefills_flush(monkeypatch):
+    """A prefill folds what is buffered first. Where it fails after that,
+    decoding goes on, and its intervals count from the empty buffer."""
+    s, flushes, _ = bare_stage(monkeypatch, 5)
+    with pytest.raises(Stop):
+        s.prefill(torch.zeros(2, 3, 64, dtype=torch.bfloat16))
+    assert flushes == [True] and s.t == s.t0 == 5
