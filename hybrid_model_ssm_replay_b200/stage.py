@@ -290,7 +290,7 @@ class HybridStage:
                 rssm.rssm_flush(st["state"], b["A"], force=True)
             self.t0 = self.t  # the buffers are empty, whatever comes of the prompt
         rows, dev = s.batch * T, u.device
-        u = u.reshape(rows, s.d_model).clone()
+        u = u.reshape(rows, s.d_model).clone(memory_format=torch.contiguous_format)
         cu = torch.arange(s.batch + 1, dtype=torch.int32, device=dev) * T
         kw = dict(dtype=torch.bfloat16, device=dev)
         n = torch.empty(rows, s.d_model, **kw)

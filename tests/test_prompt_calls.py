@@ -111,3 +111,18 @@ def test_intervals_count_from_the_prefills_flush(monkeypatch):
     with pytest.raises(Stop):
         s.prefill(torch.zeros(2, 3, 64, dtype=torch.bfloat16))
     assert flushes == [True] and s.t == s.t0 == 5
+
+
+@pytest.mark.parametrize("layout", ["transposed", "columns first", "every second column", "strided rows"])
+def test_prefill_takes_any_strides(monkeypatch, layout):
+    """The kernels need dense rows: prefill makes them of any tensor, and
+    leaves the caller's as it is."""
+    s, _, streams = bare_stage(monkeypatch, 0)
+    g = torch.Generator().manual_seed(1)
+    rn = lambda *size: torch.randn(*size, generator=g).to(torch.bfloat16)
+    u = {"transposed": lambda: rn(3, 2, 64).transpose(0, 1), "columns first": lambda: rn(64, 2, 3).permute(1, 2, 0),
+         "every second column": lambda: rn(2, 3, 128)[..., ::2], "strided rows": lambda: rn(2, 3, 128)[..., :64]}[layout]()
+    with pytest.raises(Stop):
+        s.prefill(u)
+    (got,) = streams
+    assert got.is_contiguous() and torch.equal(got.view(2, 3, 64), u) and got.data_ptr() != u.data_ptr()
