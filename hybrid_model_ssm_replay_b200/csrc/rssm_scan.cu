@@ -518,7 +518,7 @@ template <bool OUT>
 __global__ void __launch_bounds__(kSuThreads, 2)
     k_scan_umma(const ScanArgs a, const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mb,
                 const __grid_constant__ CUtensorMap mc, const __grid_constant__ CUtensorMap my, const int slices) {
-    extern __shared__ __align__(1024) unsigned char smem[];
+    extern __shared__ __align__(1024) unsigned char smem[];  // the swizzled operands lie on 1024-byte boundaries
     const int H = a.s.H, P = a.s.P, N = a.s.N, G = a.s.G;
     const int hs = blockIdx.x % (H * slices), h = hs / slices, p0 = 64 * (hs - h * slices);
     Item it;
@@ -528,10 +528,6 @@ __global__ void __launch_bounds__(kSuThreads, 2)
     const int q = warp & 3, half = warp >> 2;  // rows 32 q .., half the columns
     const int row = 32 * q + lane;          // this thread's token and state row
     const uint32_t sb = smem_u32(smem);
-    if (sb & 1023u) {  // the swizzled operands lie on 1024-byte boundaries
-        if (tid == 0) set_error(a.err, RSSM_DEVERR_TIMEOUT);
-        return;
-    }
     const uint32_t bar_in = sb + kSuBar, bar_s = bar_in + 8, bar_o = bar_in + 16, bar_y = bar_in + 24,
                    bar_u = bar_in + 32, bar_x = bar_in + 40, bar_f = bar_in + 48;
     volatile uint32_t* s_tmem = reinterpret_cast<volatile uint32_t*>(smem + kSuBar + 56);
