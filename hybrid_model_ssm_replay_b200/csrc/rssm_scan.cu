@@ -308,38 +308,43 @@ __global__ void __launch_bounds__(kThreads) k_scan(const ScanArgs a) {
 // four products with K = 128 or d_state. One CTA of 256 threads per (item,
 // head, 64 columns of its head_dim), two CTAs per SM; per block:
 //   S = C B^T          [128 t x 128 s], C and B as loaded (exact bf16);
-//   O = C h^T          [128 t x 64], the state in two bf16 parts;
+//   O = C h^T          [128 t x 64], the state in three bf16 parts;
 //   Y = M x            [128 t x 64], M in three parts, built in tensor memory
 //                      over S by the threads that own its rows, x as loaded;
 //   U = B^T [w x]      [128 n x 192], w x in three parts.
 // Thread (warp w, lane l) owns token and state row 32 (w % 4) + l and half
 // the columns (w / 4). The state stays in fp32 registers; O is read and
 // scaled, with D x added, before Y takes its place in tensor memory; U takes
-// M's. 112 KB of shared memory: C, B, x, and one buffer that holds the parts
-// of h and then, with half of C's (read by then), of w x. Each part of the
-// next block is fetched (TMA) as soon as its buffer has been read; x's buffer
-// takes the outputs to memory first. Rows past the request's end are zeroed
-// in x and B.
+// M's. 112 KB of shared memory: C, B, x, and one buffer that holds two parts
+// of h and then, with half of C's (read by then), the parts of w x. The third
+// part of h lies in x's buffer: its product goes first, and x is fetched when
+// it has been read (M is built meanwhile). Each part of the next block is
+// fetched (TMA) as soon as its buffer has been read; the outputs leave by way
+// of x's buffer and C's first half. Rows past the request's end are zeroed in
+// x and B.
 //
 // Decays. No difference of two sums of dt is formed: between two tokens of
 // the same 8 the exponent of M is the running sum of dt from s + 1 to t, and
 // else M's factor is (end of s's 8 tokens .. t) x (s + 1 .. end of s's 8
 // tokens), each the exponential of a sum of terms of one sign.
 //
-// Precision: a product of bf16 factors is exact in the fp32 sum. In two
-// parts everywhere, an output of a 512-token prompt was 1e-4 of the rms off
-// at worst and 2.3e-6 in the 2-norm; three parts (2^-26) of M and w x and
-// two (2^-18) of the state, which the next block reads from fp32 again,
-// give 3e-7.
+// Precision: a product of bf16 factors is exact in the fp32 sum, and three
+// parts leave 2^-26 of M, w x and the state. O adds its smallest part first,
+// so that its large sums take d_state / 16 steps. 2-norm of the outputs'
+// errors: 1.8e-7 to 2.3e-7 for prompts of 1 to 256 tokens from states of 0.1
+// to 10 (the rms of its elements). With the state in two parts (2^-18) that was
+// 3.4e-7 to 2.5e-6, the more the larger the state's share, and the time 3 to 6
+// % less; the third part's product takes half of that, the rest is x's later
+// fetch and the splitting.
 //
 // What bounds it. B200, 256 prompts of 512 tokens, 64 heads of 64 x 128
-// (4.87 GB, 0.74 ms at the copy rate): 1.76 ms in bursts, 2.06 ms back to back
-// under the power cap. Per block and head the tensor pipe is busy 2500 of
-// 7200 cycles, the schedulers issue in 49 % of theirs, the shared-memory data
-// pipe is busy 70 % of its (loads and stores half of it, the products'
-// operands the other); each CTA is a chain of load, S, M, Y, U and state, and
-// two CTAs (all that tensor memory and shared memory hold) overlap no more of
-// it. Steps that paid: TMA for the operands, outputs through shared memory and
+// (4.87 GB, 0.74 ms at the copy rate): 1.95 ms in bursts, 2.18 ms back to back
+// under the power cap. No pipe is full (per block and head, with the state in
+// two parts: the tensor pipe busy 2500 of 7200 cycles, the schedulers 49 % of
+// theirs, the shared-memory data pipe 70 %, loads and stores half of it, the
+// products' operands the other): each CTA is a chain of load, S, M, Y, U and
+// state, and two CTAs (all that tensor memory and shared memory hold) overlap
+// no more of it. Steps that paid: TMA for the operands, outputs through shared memory and
 // TMA instead of a row per lane (a quarter of the time), M's diagonal blocks
 // without branches, code short enough for the instruction cache, even shares
 // for the warps. Steps that did not: 512 threads at 64 registers (spills go to
@@ -354,17 +359,17 @@ __global__ void __launch_bounds__(kThreads) k_scan(const ScanArgs a) {
 constexpr int kSuTok = 128;                    // tokens per block
 constexpr int kSuThreads = 256;
 constexpr int kSuIssuer = 4;                   // two warps with less of M's lower triangle: of the products
-constexpr int kSuStorer = 5;                   // and of the second half of Y
+constexpr int kSuStorer = 5;                   // and of the second half of Y and C's first block
 constexpr uint32_t kSuBlk = kSuTok * 128u;     // 128 rows of 128 bytes, swizzled: 16 KB
 constexpr uint32_t kSuB = 0;                   // B rows, two 64-column blocks
-constexpr uint32_t kSuX = 2 * kSuBlk;          // x rows
-constexpr uint32_t kSuR = 3 * kSuBlk;          // parts of h (2) or w x (hi, mid)
+constexpr uint32_t kSuX = 2 * kSuBlk;          // h lo; x rows; outputs
+constexpr uint32_t kSuR = 3 * kSuBlk;          // h hi, mid; w x hi, mid
 constexpr uint32_t kSuC1 = 5 * kSuBlk;         // C columns 64.. ; later w x lo (right behind hi, mid)
-constexpr uint32_t kSuC0 = 6 * kSuBlk;         // C columns 0..63
+constexpr uint32_t kSuC0 = 6 * kSuBlk;         // C columns 0..63; outputs
 constexpr uint32_t kSuCol = 7 * kSuBlk;        // float [128]: dt_s exp(decay from s + 1 to the end of its 8 tokens)
 constexpr uint32_t kSuSum = kSuCol + 512;      // float [16]: dt sums of 8 tokens each
-constexpr uint32_t kSuBar = kSuSum + 64;       // 7 mbarriers, tensor-memory address
-constexpr uint32_t kSuSmem = kSuBar + 64;
+constexpr uint32_t kSuBar = kSuSum + 64;       // 8 mbarriers, tensor-memory address
+constexpr uint32_t kSuSmem = kSuBar + 80;
 constexpr uint32_t kSuCols = 256;              // tensor-memory columns
 constexpr uint32_t kTmS = 0, kTmLo = 128, kTmY = 192;  // S, then M hi, mid; M lo; O, then Y (U: 0..191)
 
@@ -529,8 +534,8 @@ __global__ void __launch_bounds__(kSuThreads, 2)
     const int row = 32 * q + lane;          // this thread's token and state row
     const uint32_t sb = smem_u32(smem);
     const uint32_t bar_in = sb + kSuBar, bar_s = bar_in + 8, bar_o = bar_in + 16, bar_y = bar_in + 24,
-                   bar_u = bar_in + 32, bar_x = bar_in + 40, bar_f = bar_in + 48;
-    volatile uint32_t* s_tmem = reinterpret_cast<volatile uint32_t*>(smem + kSuBar + 56);
+                   bar_u = bar_in + 32, bar_x = bar_in + 40, bar_f = bar_in + 48, bar_l = bar_in + 56;
+    volatile uint32_t* s_tmem = reinterpret_cast<volatile uint32_t*>(smem + kSuBar + 64);
     const bool wide = N > 64;  // B and C have a second block of 64 columns
     const uint32_t in_bytes = kSuBlk * (wide ? 2u : 1u) * (OUT ? 2u : 1u);  // B and C
     const int xx = h * P + p0, bx = g * N;
@@ -546,14 +551,17 @@ __global__ void __launch_bounds__(kSuThreads, 2)
         if (OUT && wide) su_tma(sb + kSuC1, mc, bx + 64, t, bar_in);
     };
     if (issuer && elect_one()) {
-        for (int i = 0; i < 7; ++i) mbar_init(bar_in + 8 * i, 1);
+        for (int i = 0; i < 8; ++i) mbar_init(bar_in + 8 * i, 1);
         mbar_expect_tx(bar_in, in_bytes);
         if (OUT) load_c0(it.t0);
-        load_x(it.t0);
         load_bc(it.t0);
+        if (OUT)
+            su_prefetch(mx, xx, it.t0);
+        else
+            load_x(it.t0);
     }
     if (warp == 0) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sb + kSuBar + 56),
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sb + kSuBar + 64),
                      "r"(kSuCols)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -577,17 +585,15 @@ __global__ void __launch_bounds__(kSuThreads, 2)
     auto chunk = [&](uint32_t buf, int j) {
         return reinterpret_cast<uint4*>(smem + buf + row * 128 + 16 * (j ^ (row & 7)));
     };
-    auto put_state = [&]() {  // hi and lo parts of the state, d_state row by row
+    auto put_state = [&]() {  // hi, mid and lo parts of the state, d_state row by row
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            uint32_t hi[4], lo[4];
+            uint32_t hi[4], mid[4], lo[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                hi[i] = pack_bf16(hst[4 * j + i]);
-                lo[i] = pack_bf16(sub2(hst[4 * j + i], bf2(hi[i])));
-            }
+            for (int i = 0; i < 4; ++i) split3(hst[4 * j + i], hi[i], mid[i], lo[i]);
             *chunk(kSuR, 4 * half + j) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *chunk(kSuR + kSuBlk, 4 * half + j) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            *chunk(kSuR + kSuBlk, 4 * half + j) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
+            *chunk(kSuX, 4 * half + j) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
     };
     // decays of this thread's token within its group of 8, from d
@@ -633,33 +639,30 @@ __global__ void __launch_bounds__(kSuThreads, 2)
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         su_fence_before();
         if (__syncthreads_or(timed_out)) {  // (x, where its copy is under way, lands before the CTA ends)
-            if (!OUT || t0 == it.t0) su_wait_long(bar_x, par);
+            if (!OUT) su_wait_long(bar_x, par);
             break;
         }
         // the block, its decays and the state's parts are in place
         su_fence_after();
-        if (OUT && warp == kSuStorer && t0 != it.t0) {
-            if (elect_one()) {  // Y of the block before has left x's buffer
-                asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-                load_x(t0);
-            }
-            __syncwarp();
-        }
         if (OUT && issuer) {
-            const uint64_t dB = su_desc(sb + kSuB), dR = su_desc(sb + kSuR);
+            const uint64_t dB = su_desc(sb + kSuB), dR = su_desc(sb + kSuR), dX = su_desc(sb + kSuX);
             const uint64_t dC0 = su_desc(sb + kSuC0), dC1 = su_desc(sb + kSuC1);
+            auto state_part = [&](uint64_t part, uint32_t add) {  // O, or more of it
+#pragma unroll 1
+                for (int ks = 0; ks < N / 16; ++ks)
+                    su_mma<su_idesc(64, 0, 1)>(tm + kTmY, (ks < 4 ? dC0 : dC1) + 2 * (ks & 3), part + 128 * ks,
+                                               add | (ks > 0));
+            };
             if (elect_one()) {
+                state_part(dX, 0);  // the smallest part first: the large sums take the fewest steps
+                su_commit(bar_l);
 #pragma unroll 1
                 for (int ks = 0; ks < N / 16; ++ks)
                     su_mma<su_idesc(128, 0, 0)>(tm + kTmS, (ks < 4 ? dC0 : dC1) + 2 * (ks & 3),
                                                 dB + (ks >> 2) * (kSuBlk / 16) + 2 * (ks & 3), ks > 0);
                 su_commit(bar_s);
-#pragma unroll 1
-                for (int ks = 0; ks < N / 16; ++ks) {
-                    const uint64_t c = (ks < 4 ? dC0 : dC1) + 2 * (ks & 3);
-                    su_mma<su_idesc(64, 0, 1)>(tm + kTmY, c, dR + 128 * ks, ks > 0);
-                    su_mma<su_idesc(64, 0, 1)>(tm + kTmY, c, dR + kSuBlk / 16 + 128 * ks, 1);
-                }
+                state_part(dR + kSuBlk / 16, 1);
+                state_part(dR, 1);
                 su_commit(bar_o);
                 if (more) {  // the next block on its way to L2
                     su_prefetch(mx, xx, t0 + kSuTok);
@@ -669,6 +672,9 @@ __global__ void __launch_bounds__(kSuThreads, 2)
                     if (wide) su_prefetch(mc, bx + 64, t0 + kSuTok);
                 }
             }
+            __syncwarp();
+            if (!su_wait(bar_l, par)) timed_out = true;
+            if (elect_one()) load_x(t0);  // in the place of the state's lo part
             __syncwarp();
         }
         const float4* s_sum = reinterpret_cast<const float4*>(smem + kSuSum);
@@ -798,8 +804,8 @@ __global__ void __launch_bounds__(kSuThreads, 2)
         // q, and the issuer waits on the products: the passes even that out.
         const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
         __nv_bfloat162 z = zero;  // NaN when x has a NaN or infinity
-        constexpr uint64_t kFirst = OUT ? 0x1E1A1414120E0800ull : 0x1C1814100C080400ull;  // byte w: warp w's first pass
-        constexpr uint32_t kPasses = OUT ? 0x24602468u : 0x44444444u;                      // digit w: how many
+        constexpr uint64_t kFirst = OUT ? 0x1D1914120F0B0600ull : 0x1C1814100C080400ull;  // byte w: warp w's first pass
+        constexpr uint32_t kPasses = OUT ? 0x34523456u : 0x44444444u;                      // digit w: how many
         const int first = static_cast<int>((kFirst >> (8 * warp)) & 31), passes = (kPasses >> (4 * warp)) & 15;
         if (!su_wait(bar_x, par)) timed_out = true;
 #pragma unroll 1
@@ -846,6 +852,7 @@ __global__ void __launch_bounds__(kSuThreads, 2)
             if (issuer) {
                 const uint64_t dX = su_desc(sb + kSuX);
                 if (elect_one()) {
+                    if (more) mbar_expect_tx(bar_in, in_bytes);
 #pragma unroll 1
                     for (int ks = 0; ks < kSuTok / 16; ++ks) {
                         su_mma_ts<su_idesc(64, 0, 1)>(tm + kTmY, tm + kTmS + 16 * ks, dX + 128 * ks, 1);
@@ -853,10 +860,6 @@ __global__ void __launch_bounds__(kSuThreads, 2)
                         su_mma_ts<su_idesc(64, 0, 1)>(tm + kTmY, tm + kTmLo + 8 * ks, dX + 128 * ks, 1);
                     }
                     su_commit(bar_y);
-                    if (more) {
-                        mbar_expect_tx(bar_in, in_bytes);
-                        load_c0(t0 + kSuTok);
-                    }
                 }
                 __syncwarp();
             }
@@ -916,16 +919,15 @@ __global__ void __launch_bounds__(kSuThreads, 2)
             }
             __syncwarp();
         }
-        // Y leaves by way of x's buffer, 32 columns at a time: the first half at
-        // once, the second after the state has been brought up to date (and what
-        // is fetched into the buffer next, x, is needed last)
+        // Y leaves, 32 columns by way of x's buffer and 32 by way of C's first block's
         auto half_sync = [&]() {  // the four warps of this half
             if (half == 0)
                 asm volatile("bar.sync 1, 128;" ::: "memory");
             else
                 asm volatile("bar.sync 2, 128;" ::: "memory");
         };
-        auto put_y = [&](int warp0) {
+        if (OUT) {
+            const uint32_t stage = half == 0 ? kSuX : kSuC0;
             uint32_t y[2][16];
             su_ld16(tml + kTmY + 32 * half, y[0]);
             su_ld16(tml + kTmY + 32 * half + 16, y[1]);
@@ -933,15 +935,20 @@ __global__ void __launch_bounds__(kSuThreads, 2)
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const uint32_t* v = &y[i >> 2][4 * (i & 3)];
-                *chunk(kSuX, i) = make_uint4(v[0], v[1], v[2], v[3]);
+                *chunk(stage, i) = make_uint4(v[0], v[1], v[2], v[3]);
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             half_sync();
             if (t0 + kSuTok <= it.t1) {
-                if (warp == warp0) {
+                if (warp == 0 || warp == kSuStorer) {
                     if (elect_one()) {
-                        if (pb < P) su_tma_store(my, sb + kSuX, pb, h, t0);
+                        if (pb < P) su_tma_store(my, sb + stage, pb, h, t0);
                         asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                        if (warp == 0)  // x's buffer is free
+                            asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar_f) : "memory");
+                        else if (more)
+                            load_c0(t0 + kSuTok);
                     }
                     __syncwarp();
                 }
@@ -949,25 +956,16 @@ __global__ void __launch_bounds__(kSuThreads, 2)
 #pragma unroll 1
                 for (int i = 0; i < 8; ++i) {
                     const int r = 16 * i + 4 * q + (lane >> 3), j = lane & 7;
-                    const uint4 v = *reinterpret_cast<const uint4*>(smem + kSuX + r * 128 + 16 * (j ^ (r & 7)));
+                    const uint4 v = *reinterpret_cast<const uint4*>(smem + stage + r * 128 + 16 * (j ^ (r & 7)));
                     if (t0 + r < it.t1 && pb + 4 * j < P)
                         *reinterpret_cast<uint4*>(a.y + (static_cast<size_t>(t0 + r) * H + h) * P + pb + 4 * j) = v;
                 }
-                half_sync();
             }
-        };
-        if (OUT && half == 0) put_y(0);
+        }
         if (!su_wait(bar_u, par)) timed_out = true;
         su_fence_after();
         if (issuer) {
             if (more && elect_one()) load_bc(t0 + kSuTok);  // U has read B and the parts of w x
-            __syncwarp();
-        }
-        if (OUT && warp == 0) {
-            if (elect_one()) {
-                asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-                asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar_f) : "memory");
-            }
             __syncwarp();
         }
         const float dec = su_exp2(A2 * total);
@@ -988,15 +986,10 @@ __global__ void __launch_bounds__(kSuThreads, 2)
                 hst[8 * j + i] = fma2(dec2, hst[8 * j + i], add2(two(u0), add2(two(u1), two(u2))));
             }
         }
-        if (OUT && more) put_state();
-        if (OUT && half == 1) {
+        if (OUT && more) {
             if (!su_wait(bar_f, par)) timed_out = true;
-            put_y(kSuStorer);
+            put_state();
         }
-    }
-    if (OUT && warp == kSuStorer) {
-        if (elect_one()) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-        __syncwarp();
     }
     if (timed_out) set_error(a.err, RSSM_DEVERR_TIMEOUT);
     if ((!OUT || it.last) && row < N) {
@@ -1144,16 +1137,17 @@ cudaError_t launch_pass(const ScanArgs& a, int items, cudaStream_t st) {
 // the segments' states less; two more launches cost 15 us and the join its
 // bytes. 148 SMs: the
 // workspace must not depend on the device that asks. Measured against whole
-// requests: one prompt of 8192 tokens, 64 heads, 336 -> 186 us in 4 segments;
-// 16 prompts of up to 1501 tokens, 64 heads, 118 us whole and 149 us at best
-// in segments.
+// requests: one prompt of 8192 tokens, 64 heads, 350 -> 189 us in 4 segments;
+// 16 prompts of up to 1501 tokens, 64 heads, 117 us whole and 148 us at best
+// in segments; one of 16384 tokens, 128 heads, which the model leaves whole,
+// 696 us and 647 us in 2 segments.
 int scan_segment_len(const Shape& s, int in_bf16, int total, int max_seqlen) {
     struct Cost {
         int per_sm, tok;      // CTAs that share an SM; tokens per step
         double alone, shared, state_alone, state_shared;
     };
     const bool umma = scan_umma_shape(s, in_bf16);
-    const Cost c = umma ? Cost{2, 128, 5.2, 7.7, 2.6, 3.8} : Cost{4, 128, 45, 150, 27, 80};
+    const Cost c = umma ? Cost{2, 128, 5.4, 8.1, 2.6, 3.8} : Cost{4, 128, 45, 150, 27, 80};
     const double heads = static_cast<double>(s.H) * (umma ? (s.P + 63) / 64 : 1);
     const long long longest = max_seqlen < total ? max_seqlen : total;
     const long long steps = (longest + c.tok - 1) / c.tok;

@@ -314,11 +314,12 @@ RSSM_API rssm_status_t rssm_prefill(const rssm_desc_t *desc, const rssm_state_t 
  * states from zero, then the states joined in order, then the outputs from
  * the joined states. Sums and the carried state are fp32. With bf16 inputs
  * and head_dim a multiple of 8 the products run on the tensor cores, fp32
- * factors in bf16 parts: three of the weighted x and of the products of
- * tokens (errors of 2^-26 of a term), two of the state that an output reads
- * (2^-18).
+ * factors (the weighted x, the products of tokens, the state that an output
+ * reads) in three bf16 parts: errors of 2^-26 of a term.
  * A NaN or infinity in the inputs of a token reaches that token and later
- * ones of its request (of x: in its head_dim column), none before it.
+ * ones of its request (of x: in its head_dim column), none before it. On the
+ * tensor cores an infinity may arrive as NaN, and so may a value of the state,
+ * of the weighted x or of the products of tokens past the largest bf16.
  * Requires an fp32 state (update_dtype F32, no output copy), else
  * RSSM_ERR_UNSUPPORTED; 0 <= total <= RSSM_PROMPT_TOKENS_MAX, max_seqlen >= 0. A workspace too small:
  * RSSM_ERR_CAPACITY. Device errors: pos[b] != 0; a bad cu_seqlens range or a

@@ -162,3 +162,35 @@ def test_stage_decodes_on_after_a_prefill_that_failed(monkeypatch):
         assert d.square().mean().sqrt() <= 0.01 * scale and d.max() <= 0.05 * scale, t
     for layer in st.ssm:
         assert rssm.rssm_get_error(layer["state"]) == 0
+
+
+@pytest.mark.parametrize("P,N", [(64, 128), (64, 64), (40, 32)])
+@pytest.mark.parametrize("T,scale", [(1, 1.0), (16, 10.0), (256, 10.0), (300, 1.0)])
+def test_scan_from_a_full_state(T, scale, P, N):
+    """Outputs that are mostly those of a full checkpoint, in fp32 accuracy.
+    Tolerance: the state's bf16 parts leave 2^-27 of a term, and a sum takes 3
+    N / 16 <= 24 steps of fp32, each off by at most 2^-23 of its partial sum:
+    2^-23 sqrt(24) = 5.8e-7 where they are independent, and as much again (in
+    all 1e-6, in the 2-norm) for the decays and the tokens' own products. The
+    largest by the framework's bound, 1e-4 of the rms."""
+    b, H, G = 16, 4, 2
+    g = torch.Generator(device="cuda").manual_seed(T)
+    rn = lambda *s: torch.randn(*s, generator=g, device="cuda")
+    x, B, C = rn(b * T, H, P).to(BF), rn(b * T, G, N).to(BF), rn(b * T, G, N).to(BF)
+    dt = torch.nn.functional.softplus(rn(b * T, H) - 3)
+    A, D, ckpt = -16 ** torch.rand(H, generator=g, device="cuda"), rn(H), scale * rn(b, H, P, N)
+    st, y = rssm.RssmState(rssm.make_desc(b, H, P, N, G)), torch.empty(b * T, H, P, device="cuda")
+    st.ckpt.copy_(ckpt)
+    cu = torch.arange(b + 1, dtype=torch.int32, device="cuda") * T
+    rssm.rssm_prefill_scan(st, cu, T, x, B, C, dt, A, D, y)
+    assert rssm.rssm_get_error(st) == 0
+    h, ref = ckpt.double(), []
+    X, Bd, Cd, d = (v.double().view(b, T, *v.shape[1:]) for v in (x, B, C, dt))
+    Bd, Cd = Bd.repeat_interleave(H // G, 2), Cd.repeat_interleave(H // G, 2)
+    for t in range(T):
+        h = torch.exp(d[:, t] * A.double())[..., None, None] * h + (d[:, t, :, None] * X[:, t])[..., None] * Bd[:, t, :, None]
+        ref.append((h * Cd[:, t, :, None]).sum(-1) + D.double()[:, None] * X[:, t])
+    for got, want, what in ((y.double().view(b, T, H, P), torch.stack(ref, 1), "outputs"), (st.ckpt.double(), h, "state")):
+        e = got - want
+        assert e.norm() <= 1e-6 * want.norm(), f"{what}: {float(e.norm() / want.norm()):.2e}"
+        assert e.abs().max() <= 1e-4 * want.square().mean().sqrt(), what
