@@ -338,13 +338,12 @@ __global__ void __launch_bounds__(kThreads) k_scan(const ScanArgs a) {
 // fetch and the splitting.
 //
 // What bounds it. B200, 256 prompts of 512 tokens, 64 heads of 64 x 128
-// (4.87 GB, 0.74 ms at the copy rate): 1.95 ms in bursts, 2.18 ms back to back
-// under the power cap. No pipe is full (per block and head, with the state in
-// two parts: the tensor pipe busy 2500 of 7200 cycles, the schedulers 49 % of
-// theirs, the shared-memory data pipe 70 %, loads and stores half of it, the
-// products' operands the other): each CTA is a chain of load, S, M, Y, U and
-// state, and two CTAs (all that tensor memory and shared memory hold) overlap
-// no more of it. Steps that paid: TMA for the operands, outputs through shared memory and
+// (4.87 GB, 0.74 ms at the copy rate): 2.0 ms in bursts, 2.2 ms back to back
+// under the power cap. No pipe is full (16 prompts of 1024 tokens: the tensor
+// pipe 38 % busy, the schedulers 49 %, the shared-memory data pipe 67 %, loads
+// and stores half of it, the products' operands the other): each CTA is a
+// chain of load, S, M, Y, U and state, and two CTAs (all that tensor memory
+// and shared memory hold) overlap no more of it. Steps that paid: TMA for the operands, outputs through shared memory and
 // TMA instead of a row per lane (a quarter of the time), M's diagonal blocks
 // without branches, code short enough for the instruction cache, even shares
 // for the warps. Steps that did not: 512 threads at 64 registers (spills go to

@@ -151,10 +151,12 @@ __device__ __forceinline__ int first_request(const int32_t* cu, int batch, int t
 // of four rows at work and two on their way; three CTAs of 80 registers per SM
 // (four of 64 spill: 0.660 ms for the case below, but 42 us for 16 prompts of 1
 // to 1501 tokens, where three take 38 us). B200, 256 prompts of 512 tokens,
-// 6144 channels (3.29 GB): 0.657 ms in bursts, 0.76 of the copy rate; 0.71 ms
-// with the next rows in registers, 0.77 ms with eight channels. Bound by
-// instruction issue (18 per element; 61 % busy) and the dependences of the
-// 24 warps that an SM holds.
+// 6144 channels (3.29 GB): 0.657 ms in bursts, 0.76 of the copy rate (0.69 to
+// 0.73 ms back to back); 0.71 ms with the next rows in registers, 0.77 ms with
+// eight channels. No pipe is full (issue, 18 instructions per element, is 61 %
+// busy): what is left is the dependences of the 24 warps that an SM holds. One
+// channel per thread (counts that are no multiples of 4): 64 prompts of 512
+// tokens, 63 heads, 0.76 ms, 0.17 of the copy rate.
 // ---------------------------------------------------------------------------
 // What a thread of k_conv_prompt has of its channels: VEC as one load brings
 // them, as floats, and the products.
@@ -381,7 +383,8 @@ __device__ __forceinline__ float row_sum(float v, int warps, float* red) {
 // rcp(1 + 2^(-z log2 e)) from the approximate instructions, within 2e-6 of
 // itself for |z| < 20, far inside the bf16 rounding of the result.
 // B200, 131072 rows of 4096 (8 groups; 4.29 GB): 0.69 ms, 0.96 of the copy
-// rate; 2.74 ms with one CTA per row and group that reads y and z twice.
+// rate; 2.74 ms with one CTA per row and group that reads y and z twice. 64
+// registers: 4 CTAs run per SM.
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(kNormThreads) k_gate_norm_rows(int rows, int gs, int G, int warps, size_t Dp,
                                                                  const float* __restrict__ y,
@@ -449,7 +452,10 @@ __global__ void __launch_bounds__(kNormThreads) k_gate_norm_rows(int rows, int g
     }
 }
 
-// Any other group size or row stride: one CTA per (row, group), element by element.
+// Any other group size or row stride: one CTA per (row, group), element by
+// element, y and z read twice. B200: 65536 rows of 8192 in one group 1.58 ms,
+// 0.41 of the copy rate; 133152 rows of 4032 (9 groups, rows that start on 2
+// bytes) 2.69 ms, 0.24.
 __global__ void __launch_bounds__(kNormThreads) k_gate_norm_any(int gs, int G, size_t Dp, const float* __restrict__ y,
                                                                 const __nv_bfloat16* __restrict__ zx,
                                                                 const float* __restrict__ nw, float eps,
@@ -564,7 +570,9 @@ __device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bf
 // v are read once and both sums of squares are taken from registers.
 // B200, 131072 rows of 2048, bf16 stream, every option (2.15 GB): 0.385 ms,
 // 0.85 of the copy rate (0.69 ms with the rows as floats in registers: half
-// the warps).
+// the warps); fp32 stream (3.22 GB) 0.66 ms, 0.75. Bound by L1 as much as by
+// HBM: the weights, 12 bytes an element, come from it for every row (its data
+// pipe 78 % busy, DRAM 70 %).
 // ---------------------------------------------------------------------------
 template <typename TU>
 __global__ void __launch_bounds__(512) k_add_norm_rows(const AddNormArgs a, const int warps) {
@@ -653,8 +661,9 @@ __global__ void __launch_bounds__(512) k_add_norm_rows(const AddNormArgs a, cons
 // of 8: its rows all start at the same place. A lane has one piece of a row (K =
 // 2 above 4089 elements: two) with its weights in registers for every row. The
 // next two rows are on their way to shared memory, 16 bytes at a time; the
-// pieces at a row's ends are stored in parts. Bound by instruction issue (63 %
-// busy before pairs of fp32 went through one instruction) and the two sums.
+// pieces at a row's ends are stored in parts. No pipe is full (issue was 63 %
+// busy before pairs of fp32 went through one instruction): each row waits for
+// its two sums.
 // B200: 5003 rows of 2561, fp32 stream (154 MB), 41 us, 0.57 of the copy rate;
 // 20000 of 2561, bf16, 111 us (0.57); 200000 of 1001, fp32, 0.54 ms (0.69);
 // 700000 of 257, bf16, 0.67 ms (0.33); 24000 of 8185, fp32, 0.55 ms (0.66).
@@ -662,7 +671,12 @@ __global__ void __launch_bounds__(512) k_add_norm_rows(const AddNormArgs a, cons
 // pieces in registers instead: 57 and 138 us for the first two.
 // ---------------------------------------------------------------------------
 constexpr int kShiftRows = 3;                      // rows of a team on their way or at work
-constexpr int kShiftHold = 1024;                   // threads per SM
+// Threads per SM in a grid. K = 1 (64 registers) runs them all at once. K = 2
+// (128 registers) runs one CTA per SM, and the grid is two or three rounds of
+// them: 1 to 5 % faster than one round of many rows, since a CTA's start meets
+// another's end (24000 rows of 8185, fp32: 0.565 and 0.585 ms), slower for few
+// (300 rows: 23 and 19 us).
+constexpr int kShiftHold = 1024;
 constexpr int kShiftThreads = 512;
 constexpr int kShiftDim = 16 * kShiftThreads - 7;  // two pieces per thread wherever the row starts
 
@@ -1001,8 +1015,10 @@ rssm_status_t rssm_stage_gate_norm_prompt(const rssm_desc_t* d, int32_t rows, co
         while (512 * warps < gs) warps *= 2;
         const int per_cta = kNormThreads / 32 / warps;  // teams
         // teams a multiple of G (a team keeps its group): whole rounds of G CTAs
-        // or, when a CTA has a multiple of G teams, any number of CTAs; as many
-        // as the GPU holds (8 CTAs per SM), no more than there are rows
+        // or, when a CTA has a multiple of G teams, any number of CTAs; no more
+        // than there are rows or 8 per SM, twice what runs at once (with 4 per
+        // SM: 0.663 ms for 131072 rows of 4096 in bursts either way, 17.4 us
+        // instead of 19.0 for 3000)
         const long long unit = per_cta % G == 0 ? 1 : G, rows_per_unit = unit * per_cta / G;
         const long long want = (rows + rows_per_unit - 1) / rows_per_unit;
         const long long hold = 8ll * sm_count() / unit;
@@ -1053,8 +1069,7 @@ rssm_status_t rssm_stage_add_norm(int32_t rows, int32_t dim, int32_t u_dtype, co
         const bool two = dim > 8 * kShiftThreads - 7;
         const int warps = (dim + 7 + (two ? 511 : 255)) / (two ? 512 : 256), per_cta = warps < 8 ? 8 / warps : 1;
         const int threads = 32 * warps * per_cta;
-        // teams a multiple of 8, no more than the GPU holds (a few CTAs more would run
-        // alone at the end) or there are rows
+        // teams a multiple of 8, no more than kShiftHold threads per SM or there are rows
         const long long unit = per_cta % 8 == 0 ? 1 : per_cta % 4 == 0 ? 2 : per_cta % 2 == 0 ? 4 : 8;
         const long long want = (rows - 1ll + unit * per_cta) / (unit * per_cta);
         const long long hold = static_cast<long long>(sm_count()) * (kShiftHold / threads) / unit;

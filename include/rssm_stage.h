@@ -74,8 +74,10 @@ RSSM_API rssm_status_t rssm_stage_gate_norm(const rssm_desc_t *desc, const float
  *   x [total][H][P], B and C [total][G][N] bf16; dt [total][H] float
  *   conv_state, conv_w, conv_b, dt_bias as in rssm_stage_conv
  *   err     device int32, the error word (state->err), or NULL
- * 0 <= total <= RSSM_PROMPT_TOKENS_MAX; nheads <= 2^23. Device error: a bad cu_seqlens range (RSSM_DEVERR_SEQ_RANGE;
- * that request is left untouched). */
+ * 0 <= total <= RSSM_PROMPT_TOKENS_MAX. nheads <= 2^23 and at most 65534 * 256
+ * channels (four times as many where d_inner, G N and H are multiples of 4),
+ * else RSSM_ERR_SHAPE. Device error: a bad cu_seqlens range
+ * (RSSM_DEVERR_SEQ_RANGE; that request is left untouched). */
 RSSM_API rssm_status_t rssm_stage_conv_prompt(const rssm_desc_t *desc, int32_t total, const int32_t *cu_seqlens,
                                               const void *zxbcdt, void *conv_state, const float *conv_w,
                                               const float *conv_b, const float *dt_bias, void *x, void *B,
@@ -85,7 +87,9 @@ RSSM_API rssm_status_t rssm_stage_conv_prompt(const rssm_desc_t *desc, int32_t t
  * `rows` rows (desc's batch is not used), any number of them, and any group
  * size d_inner / G.
  *   y float [rows][d_inner]; zxbcdt bf16 [rows][Dp]; norm_w float [d_inner];
- *   out bf16 [rows][d_inner]; eps > 0; rows >= 0. */
+ *   out bf16 [rows][d_inner]; eps > 0; rows >= 0. More than 65535 groups of a
+ *   size that is no multiple of 8 (or above 4096, or in rows of a Dp that is no
+ *   multiple of 8): RSSM_ERR_SHAPE. */
 RSSM_API rssm_status_t rssm_stage_gate_norm_prompt(const rssm_desc_t *desc, int32_t rows, const float *y,
                                                    const void *zxbcdt, const float *norm_w, float eps,
                                                    void *out, void *stream);
